@@ -37,6 +37,20 @@ SIGNATURES = {
     "kmeans_emeans_workspace_bytes": (_sz, [_i64, _i64, _i64, C.c_int, _i64]),
     "kmeans_emeans": (C.c_int, [_p, C.c_int, _i64, _i64, _i64, _p, _i64, _i32, C.c_double, C.c_double, C.c_double,
                                 C.c_double, _p, _p, _p, _p, _p, _p, _sz, _p]),
+    "kmeans_lookup": (C.c_int, [_p, C.c_int, _i64, _i64, _i64, _p, _i64, C.c_float, _p, _p]),
+    "kmeans_lookup_grad_workspace_bytes": (_sz, [_i64, _i64, _i64, _i64, C.c_int]),
+    "kmeans_lookup_grad": (C.c_int, [_p, C.c_int, _i64, _i64, _i64, _p, _i64, C.c_float, _p, C.c_int, _p, _sz, _p]),
+    "kmeans_dispatch_workspace_bytes": (_sz, [_i64, _i64, _i64]),
+    "kmeans_dispatch": (C.c_int, [_p, C.c_int, _i64, _i64, _p, _i64, _i64, _p, _p, _p, _p, _p, _sz, _p]),
+    "kmeans_combine": (C.c_int, [_p, C.c_int, _i64, _i64, _i64, _p, _p, _p, _p]),
+    "kmeans_combine_grad": (C.c_int, [_p, _p, C.c_int, _i64, _i64, _i64, _p, _p, _p, _p, _p, _p]),
+    "kmeans_codes_bytes": (_sz, [_i64, _i64]),
+    "kmeans_pack_codes": (C.c_int, [_p, _i64, _i64, _p, _p]),
+    "kmeans_codes_workspace_bytes": (_sz, [_i64, _i64, _i64, _i64, C.c_int]),
+    "kmeans_codes_product": (C.c_int, [_p, C.c_int, _i64, _p, _p, _i64, _p, _i64, _i64, _i64, _i64, _p, _p, _p, _sz,
+                                       _p]),
+    "kmeans_codes_product_grad": (C.c_int, [_p, C.c_int, _i64, _p, _p, _i64, _p, _i64, _i64, _i64, _i64, _p, _p, _p,
+                                            _sz, _p]),
     "kmeans_status_str": (C.c_char_p, [C.c_int]),
     "kmeans_last_error": (C.c_char_p, []),
     "kmeans_version": (C.c_int, []),

@@ -348,3 +348,241 @@ def kmeans_emeans(x, init, batch: int, epochs: int, alpha0: float, floor_frac: f
                          _ptr(labels), _ptr(counts), _ptr(objective), _ptr(ws), ws.numel(), _stream(dev))
     _lib.check(st, "kmeans_emeans")
     return centroids, labels, counts, objective
+
+
+# Labels and codebooks inside a model --------------------------------------
+# A call may be a few microseconds of GPU work, so these wrappers check each
+# tensor once and keep to the checks that the C ABI cannot make.
+
+def _tensor(t, name, dev, dtype, shape):
+    """t checked against a device, a dtype (None: any the library has) and a
+    shape (None: any); dev None: any GPU."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a GPU tensor")
+    if dev is not None and t.device != dev:
+        raise ValueError(f"{name} must be on {dev}, got {t.device}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if dtype is None:
+        if t.dtype not in _DT:
+            raise TypeError(f"{name} dtype {t.dtype} is not float32 / float16 / bfloat16")
+    elif t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    return t
+
+
+def _output(t, name, dev, dtype, shape):
+    return torch.empty(shape, dtype=dtype, device=dev) if t is None else _tensor(t, name, dev, dtype, shape)
+
+
+def _bytes(n, device):
+    return torch.empty(max(int(n), 256), dtype=torch.uint8, device=device)
+
+
+def kmeans_lookup(table, labels, scale: float = 1.0, out=None):
+    """scale * table[b, labels[b, i]] for every label: table [B, V, d], labels
+    [B, N] int32 -> [B, N, d]; labels outside [0, V) give rows of zeros."""
+    _tensor(table, "table", None, None, None)
+    if table.dim() != 3:
+        raise ValueError("table must be [B, V, d]")
+    B, V, d = table.shape
+    dev = table.device
+    _tensor(labels, "labels", dev, torch.int32, None)
+    if labels.dim() != 2 or labels.shape[0] != B:
+        raise ValueError("labels must be [B, N] int32")
+    N = labels.shape[1]
+    out = _output(out, "out", dev, table.dtype, (B, N, d))
+    st = _lib.load().kmeans_lookup(table.data_ptr(), _DT[table.dtype], B, V, d, labels.data_ptr(), N, scale,
+                                   out.data_ptr(), _stream(dev))
+    if st:
+        _lib.check(st, "kmeans_lookup")
+    return out
+
+
+def lookup_grad_workspace(B: int, N: int, d: int, V: int, dtype: torch.dtype, device) -> torch.Tensor:
+    """A workspace for kmeans_lookup_grad at these shapes."""
+    return _bytes(_lib.load().kmeans_lookup_grad_workspace_bytes(B, N, d, V, _DT[dtype]), device)
+
+
+def kmeans_lookup_grad(grad, labels, V: int, scale: float = 1.0, out=None, ws=None):
+    """Gradient of kmeans_lookup's table: scale times the sum of grad's rows
+    per label.  grad [B, N, d], labels [B, N] int32 -> [B, V, d] of grad's
+    dtype, or of out's (grad's dtype or float32)."""
+    _tensor(grad, "grad", None, None, None)
+    if grad.dim() != 3:
+        raise ValueError("grad must be [B, N, d]")
+    B, N, d = grad.shape
+    dev = grad.device
+    _tensor(labels, "labels", dev, torch.int32, (B, N))
+    if out is None:
+        out = torch.empty((B, V, d), dtype=grad.dtype, device=dev)
+    else:
+        _tensor(out, "out", dev, None, (B, V, d))
+    ws = lookup_grad_workspace(B, N, d, V, grad.dtype, dev) if ws is None else \
+        _tensor(ws, "workspace", dev, torch.uint8, None)
+    st = _lib.load().kmeans_lookup_grad(grad.data_ptr(), _DT[grad.dtype], B, N, d, labels.data_ptr(), V, scale,
+                                        out.data_ptr(), _DT[out.dtype], ws.data_ptr(), ws.numel(), _stream(dev))
+    if st:
+        _lib.check(st, "kmeans_lookup_grad")
+    return out
+
+
+def dispatch_workspace(T: int, top: int, E: int, device) -> torch.Tensor:
+    """A workspace for kmeans_dispatch at these shapes."""
+    return _bytes(_lib.load().kmeans_dispatch_workspace_bytes(T, top, E), device)
+
+
+def kmeans_dispatch(x, experts, E: int, rows=None, plan=None, ws=None):
+    """Tokens sorted by expert: x [T, d], experts [T, top] int32 (outside
+    [0, E): dropped).  Returns (rows [T * top, d], offsets [E + 1], slots
+    [T, top], order [T * top]): expert e's rows are rows[offsets[e] :
+    offsets[e + 1]], rows[slots[t, k]] = x[t], order[p] = t * top + k, and the
+    rows from offsets[E] on are zeros with order -1; dropped choices have slot
+    -1.  plan: (offsets, slots, order) tensors to write.  The gradient of x is
+    kmeans_combine(grad_rows, slots, None)."""
+    _tensor(x, "x", None, None, None)
+    if x.dim() != 2:
+        raise ValueError("x must be [T, d]")
+    T, d = x.shape
+    dev = x.device
+    _tensor(experts, "experts", dev, torch.int32, None)
+    if experts.dim() != 2 or experts.shape[0] != T:
+        raise ValueError("experts must be [T, top] int32")
+    top = experts.shape[1]
+    rows = _output(rows, "rows", dev, x.dtype, (T * top, d))
+    offsets, slots, order = (None, None, None) if plan is None else plan
+    offsets = _output(offsets, "offsets", dev, torch.int32, (E + 1,))
+    slots = _output(slots, "slots", dev, torch.int32, (T, top))
+    order = _output(order, "order", dev, torch.int32, (T * top,))
+    ws = dispatch_workspace(T, top, E, dev) if ws is None else _tensor(ws, "workspace", dev, torch.uint8, None)
+    st = _lib.load().kmeans_dispatch(x.data_ptr(), _DT[x.dtype], T, d, experts.data_ptr(), top, E, rows.data_ptr(),
+                                     offsets.data_ptr(), slots.data_ptr(), order.data_ptr(), ws.data_ptr(),
+                                     ws.numel(), _stream(dev))
+    if st:
+        _lib.check(st, "kmeans_dispatch")
+    return rows, offsets, slots, order
+
+
+def _sorted_rows(rows, slots):
+    _tensor(rows, "rows", None, None, None)
+    dev = rows.device
+    _tensor(slots, "slots", dev, torch.int32, None)
+    if slots.dim() != 2:
+        raise ValueError("slots must be [T, top] int32")
+    T, top = slots.shape
+    if rows.dim() != 2 or rows.shape[0] != T * top:
+        raise ValueError("rows must be [T * top, d]")
+    return T, top, rows.shape[1], dev
+
+
+def kmeans_combine(rows, slots, weights=None, out=None):
+    """Sorted rows back at their tokens: out[t] = sum_k weights[t, k] *
+    rows[slots[t, k]] (weights None: all 1), slots -1 adding nothing."""
+    T, top, d, dev = _sorted_rows(rows, slots)
+    if weights is not None:
+        _tensor(weights, "weights", dev, torch.float32, (T, top))
+    out = _output(out, "out", dev, rows.dtype, (T, d))
+    st = _lib.load().kmeans_combine(rows.data_ptr(), _DT[rows.dtype], T, d, top, slots.data_ptr(), _ptr(weights),
+                                    out.data_ptr(), _stream(dev))
+    if st:
+        _lib.check(st, "kmeans_combine")
+    return out
+
+
+def kmeans_combine_grad(grad, rows, slots, order, weights, grad_rows=None, grad_weights=None):
+    """Gradients of kmeans_combine: (grad_rows [T * top, d] = weights * grad at
+    every slot, zeros from offsets[E] on; grad_weights [T, top] float32 = <grad,
+    row>, 0 for a dropped choice)."""
+    T, top, d, dev = _sorted_rows(rows, slots)
+    _tensor(grad, "grad", dev, rows.dtype, (T, d))
+    _tensor(order, "order", dev, torch.int32, (T * top,))
+    _tensor(weights, "weights", dev, torch.float32, (T, top))
+    grad_rows = _output(grad_rows, "grad_rows", dev, rows.dtype, (T * top, d))
+    grad_weights = _output(grad_weights, "grad_weights", dev, torch.float32, (T, top))
+    st = _lib.load().kmeans_combine_grad(grad.data_ptr(), rows.data_ptr(), _DT[rows.dtype], T, d, top,
+                                         slots.data_ptr(), order.data_ptr(), weights.data_ptr(),
+                                         grad_rows.data_ptr(), grad_weights.data_ptr(), _stream(dev))
+    if st:
+        _lib.check(st, "kmeans_combine_grad")
+    return grad_rows, grad_weights
+
+
+def kmeans_pack_codes(labels, codes=None):
+    """4-bit labels [M, K] int32 (as kmeans_fit labels the scalar rows of a
+    weight matrix, K <= 16 clusters) laid out for kmeans_codes_product:
+    uint8 [ceil(M / 16), ceil(K / 128), 1024]."""
+    _tensor(labels, "labels", None, torch.int32, None)
+    if labels.dim() != 2:
+        raise ValueError("labels must be [M, K] int32")
+    M, K = labels.shape
+    dev = labels.device
+    codes = _output(codes, "codes", dev, torch.uint8, (-(-M // 16), -(-K // 128), 1024))
+    st = _lib.load().kmeans_pack_codes(labels.data_ptr(), M, K, codes.data_ptr(), _stream(dev))
+    if st:
+        _lib.check(st, "kmeans_pack_codes")
+    return codes
+
+
+def codes_workspace(S: int, E: int, M: int, K: int, dtype: torch.dtype, device) -> torch.Tensor:
+    """A workspace for kmeans_codes_product and kmeans_codes_product_grad at
+    these shapes."""
+    return _bytes(_lib.load().kmeans_codes_workspace_bytes(S, E, M, K, _DT[dtype]), device)
+
+
+def _codes_call(name, x, codes, table, M, K, scales, group, offsets, out, n_out, ws):
+    dev, S = x.device, x.shape[0]
+    _tensor(codes, "codes", dev, torch.uint8, None)
+    if codes.dim() == 3:
+        E = 1
+    elif codes.dim() == 4:
+        E = codes.shape[0]
+    else:
+        raise ValueError("codes must be [E, ceil(M / 16), ceil(K / 128), 1024] (or without E)")
+    if codes.shape[-3:] != (-(-M // 16), -(-K // 128), 1024):
+        raise ValueError(f"codes must be tiles {(-(-M // 16), -(-K // 128), 1024)}, got {tuple(codes.shape[-3:])}")
+    _tensor(table, "table", dev, x.dtype, None)
+    if table.dim() < 2 or table.shape[-1] != 16 or table.shape[-2] not in (1, M) or table.numel() != E * table.shape[-2] * 16:
+        raise ValueError("table must be [E, M, 16] or [E, 1, 16]")
+    if scales is not None:
+        groups = -(-K // group) if group > 0 else 0
+        _tensor(scales, "scales", dev, x.dtype, None)
+        if scales.dim() < 2 or scales.shape[-1] != groups or scales.shape[-2] != M or scales.numel() != E * M * groups:
+            raise ValueError("scales must be [E, M, ceil(K / group)]")
+    if offsets is not None:
+        _tensor(offsets, "offsets", dev, torch.int32, (E + 1,))
+    elif E != 1:
+        raise ValueError("offsets are needed for more than one expert")
+    out = _output(out, "out", dev, x.dtype, (S, n_out))
+    ws = codes_workspace(S, E, M, K, x.dtype, dev) if ws is None else _tensor(ws, "workspace", dev, torch.uint8, None)
+    st = getattr(_lib.load(), name)(x.data_ptr(), _DT[x.dtype], S, codes.data_ptr(), table.data_ptr(),
+                                    table.shape[-2], _ptr(scales), group, E, M, K, _ptr(offsets), out.data_ptr(),
+                                    ws.data_ptr(), ws.numel(), _stream(dev))
+    if st:
+        _lib.check(st, name)
+    return out
+
+
+def kmeans_codes_product(x, codes, table, M: int, scales=None, group: int = 0, offsets=None, out=None, ws=None):
+    """Rows times 4-bit matrices: out[p, m] = sum_k x[p, k] * scales[e, m, k //
+    group] * table[e, m, code[e, m, k]], e the expert whose segment
+    offsets[e] : offsets[e + 1] holds p (offsets None: one matrix).  x [S, K]
+    float16 / bfloat16, codes of kmeans_pack_codes (stacked over the experts),
+    table [E, M, 16] or [E, 1, 16] and scales [E, M, ceil(K / group)] of x's
+    dtype.  Returns [S, M]; rows past offsets[E] are zeros."""
+    _tensor(x, "x", None, None, None)
+    if x.dim() != 2:
+        raise ValueError("x must be [S, K]")
+    return _codes_call("kmeans_codes_product", x, codes, table, M, x.shape[1], scales, group, offsets, out, M, ws)
+
+
+def kmeans_codes_product_grad(grad, codes, table, K: int, scales=None, group: int = 0, offsets=None, out=None, ws=None):
+    """Gradient of kmeans_codes_product's x: grad [S, M] -> [S, K]."""
+    _tensor(grad, "grad", None, None, None)
+    if grad.dim() != 2:
+        raise ValueError("grad must be [S, M]")
+    return _codes_call("kmeans_codes_product_grad", grad, codes, table, grad.shape[1], K, scales, group, offsets, out,
+                       K, ws)

@@ -11,15 +11,13 @@
 #include <mutex>
 #include <string>
 
-#include "../../include/kmeans.h"
-#include "common.h"
+#include "host.h"
 
 namespace km {
 
 static thread_local std::string g_last_error;
 
-static km_status fail(km_status st, const char* fmt, ...) __attribute__((format(printf, 2, 3)));
-static km_status fail(km_status st, const char* fmt, ...) {
+km_status fail(km_status st, const char* fmt, ...) {
     char buf[512];
     va_list ap;
     va_start(ap, fmt);
@@ -29,11 +27,9 @@ static km_status fail(km_status st, const char* fmt, ...) {
     return st;
 }
 
-static km_status hip_fail(hipError_t e, const char* where) {
+km_status hip_fail(hipError_t e, const char* where) {
     return fail(KM_EHIP, "%s: %s", where, hipGetErrorString(e));
 }
-
-static size_t align_up(size_t v) { return (v + 255) & ~(size_t)255; }
 
 static bool use_assign_1d(int64_t d, int64_t K) { return d == 1 && assign_1d_supports(K); }
 static bool use_update_1d(DType xt, const void* x, const float* w, const int32_t* labels, int64_t d, int64_t N,
@@ -87,17 +83,6 @@ using namespace km;
 
 namespace {
 
-// The code of an enum argument as the caller passed it: a C caller may pass
-// any int, and reading a value outside the enumerators through the enum type
-// is undefined, so the bytes are read as an int.
-template <typename E>
-int enum_code(const E& e) {
-    static_assert(sizeof(E) == sizeof(int), "enums of the ABI are int-sized");
-    int v;
-    memcpy(&v, &e, sizeof v);
-    return v;
-}
-
 constexpr int64_t kMaxD = 512;     // 16-bit points
 constexpr int64_t kMaxDF32 = 256;  // float32 points
 constexpr int64_t kMaxK = 32768;
@@ -130,36 +115,7 @@ km_status check_scalar_k(int64_t d, int64_t K) {
     return KM_OK;
 }
 
-km_status need(const void* p, int64_t n, const char* name) {
-    if (n > 0 && p == nullptr) return fail(KM_EINVAL, "%s is NULL", name);
-    return KM_OK;
-}
-
-km_status check_ws(const Workspace& w, const void* ws, size_t bytes) {
-    if (w.total == 0) return KM_OK;
-    if (ws == nullptr) return fail(KM_EINVAL, "workspace is NULL (%zu bytes needed)", w.total);
-    if ((uintptr_t)ws % 256 != 0) return fail(KM_EINVAL, "workspace must be 256-byte aligned");
-    if (bytes < w.total)
-        return fail(KM_EWORKSPACE, "workspace of %zu bytes is smaller than the %zu needed", bytes, w.total);
-    return KM_OK;
-}
-
-#define KM_TRY(expr)                       \
-    do {                                   \
-        km_status _st = (expr);            \
-        if (_st != KM_OK) return _st;      \
-    } while (0)
-
-#define KM_HIP(expr, where)                              \
-    do {                                                 \
-        hipError_t _e = (expr);                          \
-        if (_e != hipSuccess) return hip_fail(_e, where); \
-    } while (0)
-
-template <typename P>
-P* at(void* ws, size_t off) {
-    return (P*)((char*)ws + off);
-}
+km_status check_ws(const Workspace& w, const void* ws, size_t bytes) { return check_ws_bytes(w.total, ws, bytes); }
 
 // Assignment of all B*N points against C; optional per-block objective
 // partials reduced into obj_out[b * obj_stride].  prep = false: the tile

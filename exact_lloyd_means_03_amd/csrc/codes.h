@@ -1,0 +1,146 @@
+// Device helpers of the products with 4-bit weights (codes.hip): decoding of
+// a word of eight codes through a 16-entry codebook in registers, the expert
+// segment a token tile belongs to, and the 16-bit matrix instructions.
+#pragma once
+
+#include "common.h"
+
+namespace km {
+
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+
+// A codebook of 16 entries of 16 bits as byte planes: low[0..3] holds the low
+// bytes of entries 0-3, 4-7, 8-11, 12-15, high[] the high bytes.
+struct Book {
+    uint32_t low[4], high[4];
+};
+
+// v_perm_b32: selector bytes 0-3 pick from b, 4-7 from a, 0x0c gives 0x00 and
+// 0x0d gives 0xff.
+__device__ __forceinline__ uint32_t perm(uint32_t a, uint32_t b, uint32_t sel) {
+    return __builtin_amdgcn_perm(a, b, sel);
+}
+
+// entries: 8 words of two entries each (16 consecutive 16-bit values).
+__device__ __forceinline__ Book make_book(const uint32_t (&w)[8]) {
+    Book k;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        k.low[i] = perm(w[2 * i + 1], w[2 * i], 0x06040200u);
+        k.high[i] = perm(w[2 * i + 1], w[2 * i], 0x07050301u);
+    }
+    return k;
+}
+
+// Four codes (the low nibble of each byte of `c`, other bits zero in bit
+// positions 0-3 only) to two words of two entries.  Bytes 0-7 of a plane come
+// from one v_perm, bytes 8-15 from another, bit 3 of the code chooses.
+__device__ __forceinline__ void decode4(const Book& k, uint32_t sel, uint32_t hi8, uint32_t* w01, uint32_t* w23) {
+    const uint32_t a = perm(k.low[1], k.low[0], sel), b = perm(k.low[3], k.low[2], sel);
+    const uint32_t c = perm(k.high[1], k.high[0], sel), d = perm(k.high[3], k.high[2], sel);
+    const uint32_t lo = (b & hi8) | (a & ~hi8), hi = (d & hi8) | (c & ~hi8);
+    *w01 = perm(hi, lo, 0x05010400u);
+    *w23 = perm(hi, lo, 0x07030602u);
+}
+
+// Eight codes of a word to eight 16-bit values in element order: the low
+// nibbles of its bytes are elements 0-3, the high nibbles elements 4-7.
+__device__ __forceinline__ u32x4 decode8(const Book& k, uint32_t w) {
+    const uint32_t e = w & 0x07070707u, o = (w >> 4) & 0x07070707u;
+    const uint32_t me = perm(0, 0, ((w >> 3) & 0x01010101u) | 0x0c0c0c0cu);
+    const uint32_t mo = perm(0, 0, ((w >> 7) & 0x01010101u) | 0x0c0c0c0cu);
+    uint32_t r0, r1, r2, r3;
+    decode4(k, e, me, &r0, &r1);
+    decode4(k, o, mo, &r2, &r3);
+    return u32x4{r0, r1, r2, r3};
+}
+
+// 16-bit element types of the products: T selects the matrix instruction.
+template <typename T>
+struct Half;
+template <>
+struct Half<_Float16> {
+    typedef _Float16 V8 __attribute__((ext_vector_type(8)));
+    static __device__ __forceinline__ f32x4 mfma(u32x4 a, u32x4 b, f32x4 c) {
+        return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
+    }
+    static __device__ __forceinline__ float f32(uint16_t v) { return (float)__builtin_bit_cast(_Float16, v); }
+    static __device__ __forceinline__ uint16_t from(float v) { return __builtin_bit_cast(uint16_t, (_Float16)v); }
+};
+template <>
+struct Half<__bf16> {
+    static __device__ __forceinline__ f32x4 mfma(u32x4 a, u32x4 b, f32x4 c) {
+        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+    }
+    static __device__ __forceinline__ float f32(uint16_t v) { return bf16_to_f32(v); }
+    static __device__ __forceinline__ uint16_t from(float v) { return __builtin_bit_cast(uint16_t, (__bf16)v); }
+};
+
+// The segment of token tile y: tiles of TT rows are numbered expert by
+// expert, an expert of n rows having ceil(n / TT) of them, and after the last
+// expert the rows past offsets[E] (expert E, whose rows become zeros).
+// Returns the expert, or -1 if there is no such tile.  Called by whole waves;
+// offsets are clamped to [0, S] and made ascending, so that no tile reaches
+// outside the rows whatever they hold.
+struct Segment {
+    int e;
+    int64_t p0;
+    int n;
+};
+__device__ __forceinline__ Segment find_segment(const int32_t* __restrict__ offsets, int64_t S, int E, int TT, int y) {
+    Segment g{-1, 0, 0};
+    if (!offsets) {
+        if ((int64_t)y * TT >= S) return g;
+        g.e = 0;
+        g.p0 = (int64_t)y * TT;
+        g.n = S - g.p0 < TT ? (int)(S - g.p0) : TT;
+        return g;
+    }
+    const int lane = threadIdx.x & 63;
+    int32_t first = 0;       // tiles of the experts before this round
+    int32_t reach = 0;       // the largest offset so far
+    for (int e0 = 0; e0 <= E; e0 += 64) {
+        const int e = e0 + lane;
+        // lane l: rows [a, z) of expert e (the tail after the last one)
+        int32_t z = e < E ? offsets[e + 1] : (int32_t)S;
+        z = z < 0 ? 0 : z > (int32_t)S ? (int32_t)S : z;
+        int32_t m = z;  // running maximum over the lanes
+#pragma unroll
+        for (int o = 1; o < 64; o <<= 1) {
+            const int32_t t = __shfl_up(m, o, 64);
+            if (lane >= o && t > m) m = t;
+        }
+        if (m < reach) m = reach;
+        int32_t a = __shfl_up(m, 1, 64);
+        if (lane == 0) a = reach;
+        const int32_t tiles = e <= E ? (m - a + TT - 1) / TT : 0;
+        int32_t incl = tiles;
+#pragma unroll
+        for (int o = 1; o < 64; o <<= 1) {
+            const int32_t t = __shfl_up(incl, o, 64);
+            if (lane >= o) incl += t;
+        }
+        const uint64_t hit = __ballot(first + incl > y);
+        if (hit) {
+            const int src = __builtin_ctzll(hit);
+            const int32_t before = first + __shfl(incl - tiles, src, 64);
+            const int32_t sa = __shfl(a, src, 64), sz = __shfl(m, src, 64);
+            g.e = e0 + src;
+            g.p0 = (int64_t)sa + (int64_t)(y - before) * TT;
+            g.n = sz - g.p0 < TT ? (int)(sz - g.p0) : TT;
+            return g;
+        }
+        first += __shfl(incl, 63, 64);
+        reach = __shfl(m, 63, 64);
+    }
+    return g;
+}
+
+// Token tiles a launch must offer for any offsets: every expert and the tail
+// may leave one tile partly filled.
+inline int64_t segment_tiles(int64_t S, int64_t E, bool offsets, int64_t TT) {
+    if (!offsets) return (S + TT - 1) / TT;
+    return (S < E + 1 ? S : E + 1) + S / TT;
+}
+
+}  // namespace km

@@ -315,4 +315,73 @@ hipError_t launch_emeans_split(double* S, double* Nc, float* C, int64_t K, int d
 hipError_t launch_emeans_final(const double* F, const double* G, int64_t K, int d, float* C, int32_t* counts,
                                hipStream_t st);
 
+// Stable sorts of labels for the row operators (label_rank.hip).
+// Column scan of histogram rows H [B][nch][K] (nch <= 256): P = exclusive
+// prefix over the chunks, counts [B][K] = totals.
+hipError_t launch_colscan(int32_t* H, int64_t B, int64_t nch, int64_t K, int32_t* P, int32_t* counts, hipStream_t s);
+int64_t rank_chunks(int64_t B, int64_t N);
+constexpr int64_t kRouteMaxE = 4096;  // eight cursor tables of a block in LDS
+// offsets [E+1], slots [M] (place of every choice, -1 outside [0, E)) and
+// order [places] of the stable sort of M choices by expert.  H and P hold
+// rank_chunks(1, M) * E ints, counts E.
+hipError_t launch_route(const int32_t* experts, int64_t M, int64_t E, int32_t* H, int32_t* P, int32_t* counts,
+                        int32_t* offsets, int32_t* slots, int32_t* order, hipStream_t s);
+
+// Sorted keys [B][N] (labels outside [0, V) as V, last) and the indices they
+// came from, ascending within a key.
+struct KeySortPlan {
+    size_t keys = 0, order = 0, keys2 = 0, order2 = 0, hist = 0, prefix = 0, counts = 0, total = 0;
+};
+KeySortPlan plan_key_sort(int64_t B, int64_t N, int64_t V);
+hipError_t launch_key_sort(const int32_t* labels, int64_t B, int64_t N, int64_t V, const KeySortPlan& p, char* ws,
+                           hipStream_t s);
+
+// Rows by label (rows.hip).
+hipError_t launch_lookup(DType xt, const void* table, int64_t B, int64_t V, int64_t d, const int32_t* labels,
+                         int64_t N, float scale, void* out, hipStream_t s);
+// Choices up to which one launch sorts and copies.
+constexpr int64_t kDispatchSmall = 4096;
+hipError_t launch_dispatch_small(DType xt, const void* x, int64_t T, int64_t d, int64_t top, const int32_t* experts,
+                                 int64_t E, void* rows, int32_t* offsets, int32_t* slots, int32_t* order,
+                                 hipStream_t s);
+hipError_t launch_dispatch_rows(DType xt, const void* x, int64_t T, int64_t d, int64_t top, const int32_t* slots,
+                                const int32_t* n_rows, void* rows, int32_t* order, hipStream_t s);
+hipError_t launch_combine(DType xt, const void* rows, int64_t T, int64_t d, int64_t top, const int32_t* slots,
+                          const float* w, void* out, hipStream_t s);
+hipError_t launch_combine_grad(DType xt, const void* gy, const void* rows, int64_t T, int64_t d, int64_t top,
+                               const int32_t* slots, const int32_t* order, const float* w, void* grows, float* gw,
+                               hipStream_t s);
+
+// Gradient of a lookup's table (lookup_grad.hip).
+struct LookupGradPlan {
+    KeySortPlan sort;
+    size_t slot = 0, total = 0;
+    int tw = 0;
+    int64_t npieces = 0;
+};
+LookupGradPlan plan_lookup_grad(int64_t B, int64_t N, int64_t d, int64_t V, DType xt);
+hipError_t launch_lookup_grad(DType xt, const void* g, int64_t B, int64_t N, int64_t d, const int32_t* labels,
+                              int64_t V, float scale, DType gt, void* out, const LookupGradPlan& p, char* ws,
+                              hipStream_t s);
+
+// Products with 4-bit weights (codes.hip).  Codes of one matrix [M, K]:
+// ceil(M / 16) x ceil(K / 128) tiles of 1 KB.
+constexpr int kCodeRows = 16, kCodeCols = 128, kCodeTile = 1024;
+inline int64_t code_tiles_m(int64_t M) { return (M + kCodeRows - 1) / kCodeRows; }
+inline int64_t code_tiles_k(int64_t K) { return (K + kCodeCols - 1) / kCodeCols; }
+hipError_t launch_pack_codes(const int32_t* labels, int64_t M, int64_t K, void* codes, hipStream_t s);
+struct CodesArgs {
+    const void* x;          // [S][K] (or the gradient [S][M])
+    const void* codes;      // [E] matrices of tiles
+    const void* table;      // [E][table_rows][16]
+    const void* scales;     // [E][M][groups] or NULL
+    const int32_t* offsets; // [E + 1] or NULL (E == 1: all rows)
+    void* out;              // [S][M] (or [S][K])
+    int64_t S, E, M, K, group, table_rows;
+};
+size_t codes_product_scratch(int64_t S, int64_t E, int64_t M, int64_t K);
+size_t codes_product_grad_scratch(int64_t S, int64_t E, int64_t M, int64_t K);
+hipError_t launch_codes_product(DType xt, const CodesArgs& a, void* ws, hipStream_t s);
+hipError_t launch_codes_product_grad(DType xt, const CodesArgs& a, void* ws, hipStream_t s);
+
 }  // namespace km

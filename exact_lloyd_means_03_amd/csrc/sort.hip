@@ -590,6 +590,13 @@ static hipError_t launch_scan(const int32_t* counts, int64_t B, int64_t K, int32
     return hipGetLastError();
 }
 
+hipError_t launch_colscan(int32_t* H, int64_t B, int64_t nch, int64_t K, int32_t* P, int32_t* counts, hipStream_t s) {
+    hipLaunchKernelGGL(k_colscan, dim3((unsigned)((K + kColBins - 1) / kColBins), (unsigned)B), dim3(kColBins * kColQ),
+                       0, s, H, nch, (int)K, P, counts, false, (const double*)nullptr, (int64_t)0, (double*)nullptr,
+                       (int64_t)0);
+    return hipGetLastError();
+}
+
 hipError_t launch_sort(const int32_t* labels, int64_t B, int64_t N, int64_t K, const SortBufs& o, int TW,
                        int64_t npieces, hipStream_t s, SortMode mode) {
     if (B == 0) return hipSuccess;

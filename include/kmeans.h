@@ -289,6 +289,129 @@ KM_API km_status kmeans_emeans(const void *x, km_dtype xt, int64_t N, int64_t d,
                         float *centroids, int32_t *labels, int32_t *counts, double *objective,
                         void *workspace, size_t workspace_bytes, km_stream stream);
 
+/* ---------------------------------------------------------------------------
+ * Labels and codebooks inside a model.
+ *
+ * What a clustering produces is used next to it: a table's rows looked up by
+ * label (a vocabulary's embedding, a codebook of kmeans_fit), tokens sorted
+ * by the expert they were assigned to, and matrices whose weights are 4-bit
+ * labels into row codebooks (kmeans_fit / kmeans_optimal_1d over scalar
+ * rows, K <= 16).  The conventions above hold, with these limits: rows of
+ * any width d >= 1, types KM_F32 / KM_F16 / KM_BF16 unless stated, and any
+ * finite, infinite or NaN values (they propagate as in the formulas).  Sums
+ * are float32 in a fixed order: equal inputs give equal bits.  Pointers need
+ * the alignment of their elements only.  Outputs must not overlap inputs.
+ */
+
+/* Rows of a table by label, scaled (an embedding lookup).
+ *   out[b][i] = scale * table[b][labels[b][i]]
+ * in float32, rounded once.
+ *   table   [B,V,d] of dtype xt, V <= 2^30.
+ *   labels  [B,N] int32; a label outside [0, V) gives a row of zeros.
+ *   out     [B,N,d] of dtype xt. */
+KM_API km_status kmeans_lookup(const void *table, km_dtype xt, int64_t B, int64_t V, int64_t d,
+                        const int32_t *labels, int64_t N, float scale, void *out, km_stream stream);
+
+/* Gradient of kmeans_lookup's table, by sorted labels.
+ *   grad_table[b][v] = scale * sum over labels[b][i] == v of grad[b][i]
+ * summed in float32 in ascending order of i within fixed pieces, rounded
+ * once; rows of labels that do not occur are zeros.  Labels outside [0, V)
+ * are skipped.
+ *   grad        [B,N,d] of dtype xt.
+ *   grad_table  out [B,V,d] of dtype gt: xt, or KM_F32.
+ * The workspace must hold kmeans_lookup_grad_workspace_bytes() bytes,
+ * 256-byte aligned (0 from the query: invalid shapes). */
+KM_API size_t kmeans_lookup_grad_workspace_bytes(int64_t B, int64_t N, int64_t d, int64_t V, km_dtype xt);
+KM_API km_status kmeans_lookup_grad(const void *grad, km_dtype xt, int64_t B, int64_t N, int64_t d,
+                             const int32_t *labels, int64_t V, float scale, void *grad_table, km_dtype gt,
+                             void *workspace, size_t workspace_bytes, km_stream stream);
+
+/* Tokens sorted by expert.  Each of T tokens has `top` choices of an expert;
+ * the T * top choices are sorted by expert, stably, and choice (t, k) takes
+ * the place slots[t][k] of the sorted rows.
+ *   x        [T,d] of dtype xt.
+ *   experts  [T,top] int32; a choice outside [0, E) is dropped (no place).
+ *   rows     out [T*top,d] of dtype xt: rows[slots[t][k]] = x[t]; the rows
+ *            from offsets[E] on are zeros.
+ *   offsets  out [E+1] int32: expert e's rows are offsets[e] .. offsets[e+1).
+ *   slots    out [T,top] int32: places, -1 for dropped choices.
+ *   order    out [T*top] int32: t * top + k of each place, -1 from
+ *            offsets[E] on.
+ * 1 <= E <= 4096, T * top < 2^31.  The workspace must hold
+ * kmeans_dispatch_workspace_bytes(T, top, E) bytes, 256-byte aligned (0 from
+ * the query: none is needed, or the shapes are invalid).
+ * The gradient of x is kmeans_combine of the rows' gradient with weights
+ * NULL. */
+KM_API size_t kmeans_dispatch_workspace_bytes(int64_t T, int64_t top, int64_t E);
+KM_API km_status kmeans_dispatch(const void *x, km_dtype xt, int64_t T, int64_t d, const int32_t *experts, int64_t top,
+                          int64_t E, void *rows, int32_t *offsets, int32_t *slots, int32_t *order,
+                          void *workspace, size_t workspace_bytes, km_stream stream);
+
+/* Sorted rows brought back to their tokens, with weights.
+ *   out[t] = sum_k weights[t][k] * rows[slots[t][k]]
+ * in float32 in the order of k, rounded once; a dropped choice adds nothing,
+ * whatever its weight.
+ *   rows     [T*top,d] of dtype xt; slots [T,top] of kmeans_dispatch.
+ *   weights  [T,top] float32, or NULL (all 1).
+ *   out      [T,d] of dtype xt. */
+KM_API km_status kmeans_combine(const void *rows, km_dtype xt, int64_t T, int64_t d, int64_t top, const int32_t *slots,
+                         const float *weights, void *out, km_stream stream);
+
+/* Gradients of kmeans_combine.
+ *   grad_rows[slots[t][k]] = weights[t][k] * grad[t]   (rounded once; rows
+ *                            from offsets[E] on are zeros)
+ *   grad_weights[t][k]     = <grad[t], rows[slots[t][k]]>   (float32; 0 for
+ *                            a dropped choice)
+ *   grad          [T,d] of dtype xt; rows [T*top,d] as given to the combine.
+ *   slots, order  of kmeans_dispatch; weights [T,top] float32.
+ *   grad_rows     out [T*top,d] of dtype xt.
+ *   grad_weights  out [T,top] float32. */
+KM_API km_status kmeans_combine_grad(const void *grad, const void *rows, km_dtype xt, int64_t T, int64_t d, int64_t top,
+                              const int32_t *slots, const int32_t *order, const float *weights,
+                              void *grad_rows, float *grad_weights, km_stream stream);
+
+/* 4-bit labels of a weight matrix laid out for the products below.
+ *   labels  [M,K] int32 in [0, 16) (the low four bits are taken).
+ *   codes   out kmeans_codes_bytes(M, K) bytes, 16-byte aligned: tiles of 16
+ *           rows by 128 columns, 1024 bytes each, row of tiles by row of
+ *           tiles; absent rows and columns are code 0.  Inside a tile the
+ *           code of row r, column 32 j + 8 q + i (j, q < 4, i < 8) is in the
+ *           32-bit word (16 q + r) * 4 + j, bits 8 (i % 4) + 4 (i / 4).
+ *           0 from the query: invalid shapes. */
+KM_API size_t kmeans_codes_bytes(int64_t M, int64_t K);
+KM_API km_status kmeans_pack_codes(const int32_t *labels, int64_t M, int64_t K, void *codes, km_stream stream);
+
+/* Products of rows with 4-bit weight matrices, one matrix per expert.  The
+ * weight of expert e is
+ *   W[e][m][k] = scales[e][m][k / group] * table[e][m][code[e][m][k]]
+ * and row p of the segment offsets[e] <= p < offsets[e+1] is multiplied by
+ * its expert's matrix:
+ *   kmeans_codes_product        out[p][m] = sum_k x[p][k] W[e][m][k]
+ *   kmeans_codes_product_grad   out[p][k] = sum_m x[p][m] W[e][m][k]
+ * (the second is the gradient of the first's x).  Rows past offsets[E] become
+ * zeros.  Sums are float32, rounded once at the end.
+ *   x        [S,K] (grad: [S,M]) of dtype xt: KM_F16 or KM_BF16.
+ *   codes    E matrices of kmeans_codes_bytes(M, K) bytes, 16-byte aligned.
+ *   table    [E,table_rows,16] of dtype xt: a codebook per row (table_rows ==
+ *            M) or one per matrix (table_rows == 1).
+ *   scales   [E,M,ceil(K/group)] of dtype xt, or NULL (group is then
+ *            ignored).  group: 32, 64, or a multiple of 128.
+ *   offsets  [E+1] int32, ascending from 0, offsets[E] <= S; NULL with E == 1
+ *            means all S rows.
+ *   out      [S,M] (grad: [S,K]) of dtype xt.
+ * S < 2^31, E <= 4096, M, K <= 2^20.  The workspace must hold
+ * kmeans_codes_workspace_bytes(S, E, M, K, xt) bytes, 256-byte aligned (0
+ * from the query: none is needed, or the shapes are invalid). */
+KM_API size_t kmeans_codes_workspace_bytes(int64_t S, int64_t E, int64_t M, int64_t K, km_dtype xt);
+KM_API km_status kmeans_codes_product(const void *x, km_dtype xt, int64_t S, const void *codes, const void *table,
+                               int64_t table_rows, const void *scales, int64_t group, int64_t E, int64_t M,
+                               int64_t K, const int32_t *offsets, void *out, void *workspace,
+                               size_t workspace_bytes, km_stream stream);
+KM_API km_status kmeans_codes_product_grad(const void *grad, km_dtype xt, int64_t S, const void *codes,
+                                    const void *table, int64_t table_rows, const void *scales, int64_t group,
+                                    int64_t E, int64_t M, int64_t K, const int32_t *offsets, void *out,
+                                    void *workspace, size_t workspace_bytes, km_stream stream);
+
 /* Static description of a status code. */
 KM_API const char *kmeans_status_str(km_status status);
 
