@@ -161,24 +161,6 @@ struct AssignCfg {
     static_assert(2 * TILE <= 150 * 1024, "two tile buffers fit in LDS");
 };
 
-constexpr uint32_t vmcnt_imm(int n) {  // s_waitcnt with only vmcnt <= n
-    return (uint32_t)((n & 15) | ((n >> 4) << 14) | (7 << 4) | (15 << 8));
-}
-
-// One global_load_lds_dwordx4: lane l copies 16 bytes from sbase + voff to
-// LDS byte lds + 16 l (sbase and lds are wave-uniform: an SGPR pair and M0).
-// Written as a one-instruction asm statement so the compiler does not treat
-// the in-flight LDS write as aliasing every later LDS read (it would wait for
-// the copy right after issuing it); the kernel waits on vmcnt explicitly
-// before the barrier that publishes a tile.  The instruction has no register
-// results.
-__device__ __forceinline__ void dma16(const char* sbase, uint32_t voff, const void* lds) {
-    const uint32_t l = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) void*)lds;
-    asm volatile("global_load_lds_dwordx4 %0, %1" ::"v"(voff), "s"(sbase),
-                 "{m0}"(__builtin_amdgcn_readfirstlane(l))
-                 : "memory");
-}
-
 // LDS chunk position of global 16-byte chunk c of tile row r.  Rows of a
 // power-of-two number of chunks are XOR-swizzled, c ^ (r % SW) with SW =
 // min(chunks per row, 32), so the 32 rows read by one A-operand instruction

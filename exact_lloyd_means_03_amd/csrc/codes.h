@@ -32,27 +32,33 @@ __device__ __forceinline__ Book make_book(const uint32_t (&w)[8]) {
     return k;
 }
 
-// Four codes (the low nibble of each byte of `c`, other bits zero in bit
-// positions 0-3 only) to two words of two entries.  Bytes 0-7 of a plane come
-// from one v_perm, bytes 8-15 from another, bit 3 of the code chooses.
-__device__ __forceinline__ void decode4(const Book& k, uint32_t sel, uint32_t hi8, uint32_t* w01, uint32_t* w23) {
+// Four codes, in bits 0-2 of the bytes of sel with bit 3 as the byte masks
+// hi8, to the four low and the four high bytes of their entries: entries 0-7
+// come from one v_perm of a plane, 8-15 from another, bit 3 of the code
+// chooses.
+__device__ __forceinline__ void decode4(const Book& k, uint32_t sel, uint32_t hi8, uint32_t* lo, uint32_t* hi) {
     const uint32_t a = perm(k.low[1], k.low[0], sel), b = perm(k.low[3], k.low[2], sel);
     const uint32_t c = perm(k.high[1], k.high[0], sel), d = perm(k.high[3], k.high[2], sel);
-    const uint32_t lo = (b & hi8) | (a & ~hi8), hi = (d & hi8) | (c & ~hi8);
-    *w01 = perm(hi, lo, 0x05010400u);
-    *w23 = perm(hi, lo, 0x07030602u);
+    *lo = (b & hi8) | (a & ~hi8);
+    *hi = (d & hi8) | (c & ~hi8);
 }
 
-// Eight codes of a word to eight 16-bit values in element order: the low
-// nibbles of its bytes are elements 0-3, the high nibbles elements 4-7.
-__device__ __forceinline__ u32x4 decode8(const Book& k, uint32_t w) {
+// The byte planes of a word's eight codes: the low nibbles of its bytes are
+// elements 0-3 (lo[0], hi[0]), the high nibbles elements 4-7.
+__device__ __forceinline__ void decode_planes(const Book& k, uint32_t w, uint32_t (&lo)[2], uint32_t (&hi)[2]) {
     const uint32_t e = w & 0x07070707u, o = (w >> 4) & 0x07070707u;
     const uint32_t me = perm(0, 0, ((w >> 3) & 0x01010101u) | 0x0c0c0c0cu);
     const uint32_t mo = perm(0, 0, ((w >> 7) & 0x01010101u) | 0x0c0c0c0cu);
-    uint32_t r0, r1, r2, r3;
-    decode4(k, e, me, &r0, &r1);
-    decode4(k, o, mo, &r2, &r3);
-    return u32x4{r0, r1, r2, r3};
+    decode4(k, e, me, &lo[0], &hi[0]);
+    decode4(k, o, mo, &lo[1], &hi[1]);
+}
+
+// Eight codes of a word to eight 16-bit values in element order.
+__device__ __forceinline__ u32x4 decode8(const Book& k, uint32_t w) {
+    uint32_t lo[2], hi[2];
+    decode_planes(k, w, lo, hi);
+    return u32x4{perm(hi[0], lo[0], 0x05010400u), perm(hi[0], lo[0], 0x07030602u), perm(hi[1], lo[1], 0x05010400u),
+                 perm(hi[1], lo[1], 0x07030602u)};
 }
 
 // 16-bit element types of the products: T selects the matrix instruction.
@@ -66,6 +72,11 @@ struct Half<_Float16> {
     }
     static __device__ __forceinline__ float f32(uint16_t v) { return (float)__builtin_bit_cast(_Float16, v); }
     static __device__ __forceinline__ uint16_t from(float v) { return __builtin_bit_cast(uint16_t, (_Float16)v); }
+    // the eight values of a word times s, each product rounded once
+    static __device__ __forceinline__ u32x4 decode_scaled(const Book& k, uint32_t w, uint16_t s) {
+        typedef _Float16 H8 __attribute__((ext_vector_type(8)));
+        return __builtin_bit_cast(u32x4, __builtin_bit_cast(H8, decode8(k, w)) * (H8)__builtin_bit_cast(_Float16, s));
+    }
 };
 template <>
 struct Half<__bf16> {
@@ -74,6 +85,23 @@ struct Half<__bf16> {
     }
     static __device__ __forceinline__ float f32(uint16_t v) { return bf16_to_f32(v); }
     static __device__ __forceinline__ uint16_t from(float v) { return __builtin_bit_cast(uint16_t, (__bf16)v); }
+    static __device__ __forceinline__ u32x4 decode_scaled(const Book& k, uint32_t w, uint16_t s) {
+        typedef float F2 __attribute__((ext_vector_type(2)));
+        typedef __bf16 B2 __attribute__((ext_vector_type(2)));
+        uint32_t lo[2], hi[2];
+        decode_planes(k, w, lo, hi);
+        const float f = bf16_to_f32(s);
+        u32x4 r;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            // bytes to the float32 of elements 2 i and 2 i + 1 (0x0c: zero)
+            const uint32_t even = i & 1 ? 0x06020c0cu : 0x04000c0cu, odd = i & 1 ? 0x07030c0cu : 0x05010c0cu;
+            const F2 v = {f * __uint_as_float(perm(hi[i / 2], lo[i / 2], even)),
+                          f * __uint_as_float(perm(hi[i / 2], lo[i / 2], odd))};
+            r[i] = __builtin_bit_cast(uint32_t, __builtin_convertvector(v, B2));
+        }
+        return r;
+    }
 };
 
 // The segment of token tile y: tiles of TT rows are numbered expert by
@@ -125,9 +153,12 @@ __device__ __forceinline__ Segment find_segment(const int32_t* __restrict__ offs
             const int src = __builtin_ctzll(hit);
             const int32_t before = first + __shfl(incl - tiles, src, 64);
             const int32_t sa = __shfl(a, src, 64), sz = __shfl(m, src, 64);
-            g.e = e0 + src;
-            g.p0 = (int64_t)sa + (int64_t)(y - before) * TT;
-            g.n = sz - g.p0 < TT ? (int)(sz - g.p0) : TT;
+            // (uniform values: kept in scalar registers)
+            const int32_t p0 = __builtin_amdgcn_readfirstlane(sa + (y - before) * TT);
+            const int32_t n = __builtin_amdgcn_readfirstlane(sz) - p0;
+            g.e = __builtin_amdgcn_readfirstlane(e0 + src);
+            g.p0 = p0;
+            g.n = n < TT ? n : TT;
             return g;
         }
         first += __shfl(incl, 63, 64);

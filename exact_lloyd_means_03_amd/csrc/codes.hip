@@ -32,30 +32,42 @@ hipError_t launch_pack_codes(const int32_t* labels, int64_t M, int64_t K, void* 
     return hipGetLastError();
 }
 
-// The codebook of row m of a matrix.
-__device__ __forceinline__ Book load_book(const uint16_t* __restrict__ table, int64_t rows, int64_t m) {
-    const uint32_t* t = (const uint32_t*)(table + (rows == 1 ? 0 : m) * 16);
-    uint32_t w[8];
-    if (((uintptr_t)table & 3) == 0) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) w[i] = t[i];
-    } else {
-        const uint16_t* h = (const uint16_t*)t;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) w[i] = (uint32_t)h[2 * i] | (uint32_t)h[2 * i + 1] << 16;
-    }
+template <bool V>
+struct Tag {
+    static constexpr bool value = V;
+};
+
+// The codebook of row m of a matrix: 16 consecutive values, as two vectors.
+typedef u32x4 u32x4_any __attribute__((aligned(2)));
+__device__ __forceinline__ void fetch_book(const uint16_t* __restrict__ table, int64_t rows, int64_t m, u32x4* a,
+                                           u32x4* b) {
+    const u32x4_any* t = (const u32x4_any*)(table + (rows == 1 ? 0 : m) * 16);
+    *a = t[0];
+    *b = t[1];
+}
+__device__ __forceinline__ Book make_book(u32x4 a, u32x4 b) {
+    const uint32_t w[8] = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
     return make_book(w);
 }
+__device__ __forceinline__ Book load_book(const uint16_t* __restrict__ table, int64_t rows, int64_t m) {
+    u32x4 a, b;
+    fetch_book(table, rows, m, &a, &b);
+    return make_book(a, b);
+}
 
-// Eight consecutive 16-bit values at p, those from index n on as zero.
-__device__ __forceinline__ u32x4 load8(const uint16_t* __restrict__ p, int n) {
-    typedef u32x4 U __attribute__((aligned(2)));
-    if (n >= 8) return *(const U*)p;
-    uint32_t w[4] = {0, 0, 0, 0};
+// Eight consecutive 16-bit values of a row.
+__device__ __forceinline__ u32x4 load8(const uint16_t* __restrict__ p) { return *(const u32x4_any*)p; }
+
+// The same where only p[i], i < n, are in the row (n may be negative, but
+// p[n - 1] is the row's last element): the others as zero.
+__device__ __forceinline__ u32x4 load8_end(const uint16_t* __restrict__ p, int n) {
+    uint32_t v[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-        if (i < n) w[i / 2] |= (uint32_t)p[i] << (16 * (i & 1));
-    return u32x4{w[0], w[1], w[2], w[3]};
+    for (int i = 0; i < 8; ++i) {
+        const uint16_t e = p[i < n ? i : n - 1];
+        v[i] = i < n ? e : 0u;
+    }
+    return u32x4{v[0] | v[1] << 16, v[2] | v[3] << 16, v[4] | v[5] << 16, v[6] | v[7] << 16};
 }
 
 // The first n of eight values, the others zero.
@@ -64,6 +76,23 @@ __device__ __forceinline__ u32x4 keep8(u32x4 v, int n) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) r[i] = n >= 2 * i + 2 ? v[i] : n == 2 * i + 1 ? v[i] & 0xffffu : 0u;
     return r;
+}
+
+// Four consecutive results, the first n (>= 1) of which are in the row.
+template <typename T>
+__device__ __forceinline__ void store4(uint16_t* __restrict__ to, int64_t n, f32x4 v) {
+    typedef uint16_t u16x4 __attribute__((ext_vector_type(4)));
+    typedef u16x4 u16x4_any __attribute__((aligned(2)));
+    u16x4 h;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) h[e] = Half<T>::from(v[e]);
+    if (n >= 4) {
+        *(u16x4_any*)to = h;
+    } else {
+#pragma unroll
+        for (int e = 0; e < 3; ++e)
+            if (e < n) to[e] = h[e];
+    }
 }
 
 // ---------------------------------------------------------------------------
@@ -113,15 +142,18 @@ __global__ __launch_bounds__(64 * kProdWaves) void k_codes_product(
         }
         const int64_t mr = mt * 16 + r < M ? mt * 16 + r : M - 1;
         const Book book = load_book(table + (int64_t)g.e * table_rows * 16, table_rows, mr);
-        for (int64_t kt = w; kt < KT; kt += kProdWaves) {
+        // one tile; END: the last one of a row that is no multiple of 128 columns, of which `left` are there
+        auto tile = [&](int64_t kt, auto end_tag, int left) {
+            constexpr bool END = decltype(end_tag)::value;
             const u32x4 cw = *(const u32x4*)(cm + kt * kCodeTile);
-            const int left = (int)(K - kt * kCodeCols < kCodeCols ? K - kt * kCodeCols : kCodeCols);
             u32x4 xv[NT][4];
 #pragma unroll
             for (int n = 0; n < NT; ++n)
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    xv[n][j] = load8(xr[n] + kt * kCodeCols + j * 32, left == kCodeCols ? 8 : left - j * 32 - q * 8);
+                for (int j = 0; j < 4; ++j) {
+                    const uint16_t* p = xr[n] + kt * kCodeCols + j * 32;
+                    xv[n][j] = END ? load8_end(p, left - j * 32 - q * 8) : load8(p);
+                }
             float sv[4][GS ? GS : 1];
             if (GS) {
 #pragma unroll
@@ -137,7 +169,7 @@ __global__ __launch_bounds__(64 * kProdWaves) void k_codes_product(
             for (int j = 0; j < 4; ++j) {
                 u32x4 a = decode8(book, cw[j]);
                 // columns past the row's end: x is zero there, and so must the weight be (0 * inf is no zero)
-                if (left != kCodeCols) a = keep8(a, left - j * 32 - q * 8);
+                if (END) a = keep8(a, left - j * 32 - q * 8);
                 const bool start = GS && j % (4 / (GS ? GS : 1)) == 0;
                 const bool end = GS && (j + 1) % (4 / (GS ? GS : 1)) == 0;
 #pragma unroll
@@ -154,7 +186,10 @@ __global__ __launch_bounds__(64 * kProdWaves) void k_codes_product(
                     }
                 }
             }
-        }
+        };
+        const int64_t whole = K / kCodeCols;
+        for (int64_t kt = w; kt < whole; kt += kProdWaves) tile(kt, Tag<false>{}, 0);
+        if (whole < KT && whole % kProdWaves == w) tile(whole, Tag<true>{}, (int)(K - whole * kCodeCols));
     }
 #pragma unroll
     for (int n = 0; n < NT; ++n) s_acc[w][n][lane] = acc[n];
@@ -166,11 +201,181 @@ __global__ __launch_bounds__(64 * kProdWaves) void k_codes_product(
         for (int o = 1; o < kProdWaves; ++o) v += s_acc[o][n][l];
         const int t = n * 16 + (l & 15);
         const int64_t m = mt * 16 + (l >> 4) * 4;
-        if (t < g.n) {
-            uint16_t* to = out + (g.p0 + t) * M + m;
+        if (t < g.n && m < M) store4<T>(out + (g.p0 + t) * M + m, M - m, v);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Many rows per expert: a block of four waves takes 256 rows of the matrix by
+// 16 NT tokens.  Each wave decodes its own 64 rows, straight from the codes to
+// A operands as above, and multiplies them with every token of the block; so
+// a weight is decoded once per block and never stored.  The tokens' tile (16
+// NT rows of 128 columns, two buffers) comes to LDS by direct loads, its
+// 16-byte chunks XOR-swizzled by the row so that the 16 rows a B operand
+// reads lie on distinct banks.
+#ifndef GOCC
+#define GOCC 2
+#define GNT 6
+#define GSB 1
+#endif
+constexpr int kGemmWaves = 4, kGemmR = 4, kGemmOcc = GOCC, kGemmNT = GNT;  // waves, row tiles per wave
+
+template <typename T, int NT, int GS>
+__global__ __launch_bounds__(64 * kGemmWaves, kGemmOcc) void k_codes_gemm(
+    const uint16_t* __restrict__ x, int64_t S, const char* __restrict__ codes, const uint16_t* __restrict__ table,
+    int64_t table_rows, const uint16_t* __restrict__ scales, int64_t group, int64_t groups, int E, int64_t M,
+    int64_t K, int64_t MT, int64_t KT, const int32_t* __restrict__ offsets, uint16_t* __restrict__ out) {
+    typedef Half<T> H;
+    constexpr int R = kGemmR, TT = 16 * NT, ROW = kCodeCols * 2;
+    __shared__ __attribute__((aligned(16))) char s_x[2][TT * ROW];
+    __shared__ __attribute__((aligned(16))) uint32_t s_book[kGemmWaves * R * 16][8];
+    __shared__ __attribute__((aligned(16))) float s_scale[kGemmWaves][GS ? GS : 1][64];
+    const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+    const int r = lane & 15, q = lane >> 4;
+    const Segment g = find_segment(offsets, S, E, TT, blockIdx.y);
+    if (g.e < 0) return;
+    const int64_t mt0 = ((int64_t)blockIdx.x * kGemmWaves + w) * R;  // the wave's first row tile
+    f32x4 acc[R][NT];
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-                if (m + e < M) to[e] = H::from(v[e]);
+    for (int a = 0; a < R; ++a)
+#pragma unroll
+        for (int n = 0; n < NT; ++n) acc[a][n] = f32x4{0.f, 0.f, 0.f, 0.f};
+    if (g.e < E) {  // (block-uniform; expert E stands for the rows past the last expert's)
+        const char* xs = (const char*)(x + g.p0 * K);
+        // instruction i of the wave copies 1 KB: 4 token rows of 16 chunks
+        auto dma = [&](int64_t kt, int buf) {
+#pragma unroll
+            for (int i = 0; i < TT / 4 / kGemmWaves; ++i) {
+                const int t0 = (i * kGemmWaves + w) * 4;
+                const int t = t0 + (lane >> 4);
+                const int src = t < g.n ? t : g.n - 1;
+                const uint32_t off = (uint32_t)(src * K * 2 + kt * ROW + (((lane & 15) ^ (t & 15)) * 16));
+                dma16(xs, off, s_x[buf] + t0 * ROW);
+            }
+        };
+        // the last tile of a row that is no multiple of 128 columns: zeros past the row
+        auto copy_end = [&](int64_t kt, int buf) {
+            for (int i = threadIdx.x; i < TT * 16; i += 64 * kGemmWaves) {
+                const int t = i >> 4, c = i & 15;
+                const int src = t < g.n ? t : g.n - 1;
+                const int64_t k = kt * kCodeCols + c * 8;
+                *(u32x4*)(s_x[buf] + t * ROW + ((c ^ (t & 15)) * 16)) =
+                    load8_end((const uint16_t*)xs + src * K + k, (int)(K - k));
+            }
+        };
+        const int64_t whole = K / kCodeCols;
+        if (whole > 0) dma(0, 0);
+        const char* cm[R];
+#pragma unroll
+        for (int a = 0; a < R; ++a) {
+            const int64_t mt = mt0 + a < MT ? mt0 + a : MT - 1;  // absent tiles repeat the last one
+            cm[a] = codes + ((int64_t)g.e * MT + mt) * KT * kCodeTile + lane * 16;
+            if (q == 0) {
+                const int64_t m = mt * 16 + r < M ? mt * 16 + r : M - 1;
+                const Book b = load_book(table + (int64_t)g.e * table_rows * 16, table_rows, m);
+                uint32_t* to = s_book[(w * R + a) * 16 + r];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    to[i] = b.low[i];
+                    to[4 + i] = b.high[i];
+                }
+            }
+        }
+        u32x4 cw[R];
+#pragma unroll
+        for (int a = 0; a < R; ++a) cw[a] = *(const u32x4*)cm[a];
+        uint16_t sraw[GS ? GS : 1];
+        const int64_t ms = mt0 * 16 + lane < M ? mt0 * 16 + lane : M - 1;
+        const uint16_t* srow = GS ? scales + ((int64_t)g.e * M + ms) * groups : nullptr;
+        auto get_scales = [&](int64_t kt) {
+#pragma unroll
+            for (int h = 0; h < GS; ++h) {
+                int64_t gi = GS == 4 ? kt * 4 + h : GS == 2 ? kt * 2 + h : kt * kCodeCols / group;
+                if (gi >= groups) gi = groups - 1;
+                sraw[h] = srow[gi];
+            }
+        };
+        if (GS) get_scales(0);
+        __builtin_amdgcn_s_waitcnt(vmcnt_imm(0));
+        __syncthreads();
+        auto tile = [&](int64_t kt, int64_t next, int buf, auto end_tag) {
+            constexpr bool END = decltype(end_tag)::value;
+            // lane l's row: this tile's scales to the wave's slab, the next tile's requested
+            if (GS) {
+#pragma unroll
+                for (int h = 0; h < GS; ++h) s_scale[w][h][lane] = H::f32(sraw[h]);
+                get_scales(next);
+            }
+            const int left = (int)(K - kt * kCodeCols);
+            u32x4 av[R][4];
+#pragma unroll
+            for (int a = 0; a < R; ++a) {
+                Book b;
+                const u32x4* bp = (const u32x4*)s_book[(w * R + a) * 16 + r];
+                *(u32x4*)b.low = bp[0];
+                *(u32x4*)b.high = bp[1];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    av[a][j] = decode8(b, cw[a][j]);
+                    if (END) av[a][j] = keep8(av[a][j], left - j * 32 - q * 8);
+                }
+            }
+#pragma unroll
+            for (int a = 0; a < R; ++a) cw[a] = *(const u32x4*)(cm[a] + next * kCodeTile);
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                if (GSB) __builtin_amdgcn_sched_barrier(0);
+                u32x4 xv[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    xv[j] = *(const u32x4*)(s_x[buf] + (n * 16 + r) * ROW + (((j * 4 + q) ^ r) * 16));
+                f32x4 part[R];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const bool start = GS && j % (4 / (GS ? GS : 1)) == 0;
+                    const bool end = GS && (j + 1) % (4 / (GS ? GS : 1)) == 0;
+#pragma unroll
+                    for (int a = 0; a < R; ++a) {
+                        if (!GS) {
+                            acc[a][n] = H::mfma(av[a][j], xv[j], acc[a][n]);
+                        } else {
+                            part[a] = H::mfma(av[a][j], xv[j], start ? f32x4{0.f, 0.f, 0.f, 0.f} : part[a]);
+                        }
+                    }
+                    if (end) {
+#pragma unroll
+                        for (int a = 0; a < R; ++a) {
+                            const f32x4 sv = *(const f32x4*)&s_scale[w][j * (GS ? GS : 1) / 4][a * 16 + q * 4];
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) acc[a][n][i] = fmaf(sv[i], part[a][i], acc[a][n][i]);
+                        }
+                    }
+                }
+            }
+        };
+        for (int64_t kt = 0; kt < whole; ++kt) {
+            const int buf = (int)(kt & 1);
+            if (kt + 1 < whole) dma(kt + 1, buf ^ 1);
+            tile(kt, kt + 1 < KT ? kt + 1 : kt, buf, Tag<false>{});
+            // the next tile has landed before the barrier that publishes it
+            __builtin_amdgcn_s_waitcnt(vmcnt_imm(0));
+            __syncthreads();
+        }
+        if (whole < KT) {
+            copy_end(whole, 0);
+            __syncthreads();
+            tile(whole, whole, 0, Tag<true>{});
+        }
+    }
+#pragma unroll
+    for (int a = 0; a < R; ++a) {
+        const int64_t m = (mt0 + a) * 16 + q * 4;
+        if (m >= M) continue;
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            const int t = n * 16 + r;
+            if (t >= g.n) continue;
+            store4<T>(out + (g.p0 + t) * M + m, M - m, acc[a][n]);
         }
     }
 }
@@ -188,6 +393,14 @@ static hipError_t product_launch(const CodesArgs& a, hipStream_t s) {
     const int64_t MT = code_tiles_m(a.M), KT = code_tiles_k(a.K);
     const int64_t groups = a.scales ? (a.K + a.group - 1) / a.group : 0;
     const bool few = a.S <= 16 * a.E;
+    const bool many = a.S >= 64 * a.E && a.K % 8 == 0 && (uintptr_t)a.x % 16 == 0;
+#define KM_MANY(GS)                                                                                                  \
+    hipLaunchKernelGGL((k_codes_gemm<T, kGemmNT, GS>),                                                                     \
+                       dim3((unsigned)((MT + kGemmWaves * kGemmR - 1) / (kGemmWaves * kGemmR)),                      \
+                            (unsigned)segment_tiles(a.S, a.E, a.offsets, 16 * kGemmNT)),                                    \
+                       dim3(64 * kGemmWaves), 0, s, (const uint16_t*)a.x, a.S, (const char*)a.codes,                 \
+                       (const uint16_t*)a.table, a.table_rows, (const uint16_t*)a.scales, a.group, groups, (int)a.E, \
+                       a.M, a.K, MT, KT, a.offsets, (uint16_t*)a.out)
 #define KM_GO(NT, GS)                                                                                                \
     hipLaunchKernelGGL((k_codes_product<T, NT, GS>),                                                                 \
                        dim3((unsigned)MT, (unsigned)segment_tiles(a.S, a.E, a.offsets, 16 * NT)),                    \
@@ -197,6 +410,7 @@ static hipError_t product_launch(const CodesArgs& a, hipStream_t s) {
 #define KM_NT(GS)           \
     do {                    \
         if (few) KM_GO(1, GS); \
+        else if (many) KM_MANY(GS); \
         else KM_GO(4, GS);  \
     } while (0)
     switch (groups_per_tile(a)) {
@@ -206,6 +420,7 @@ static hipError_t product_launch(const CodesArgs& a, hipStream_t s) {
         default: KM_NT(4); break;
     }
 #undef KM_NT
+#undef KM_MANY
 #undef KM_GO
     return hipGetLastError();
 }
@@ -220,137 +435,281 @@ hipError_t launch_codes_product(DType xt, const CodesArgs& a, void*, hipStream_t
 //
 // The reduction runs over the rows of the matrix, so the A operand wants
 // eight rows of one column per lane where a lane decodes eight columns of one
-// row.  A wave decodes 32 rows by 128 columns (two tiles), multiplies by the
-// scales, stores them transposed in its own LDS slab and reads operands back.
-// Scaled weights are rounded to the 16-bit type there: a scale varies along
-// the reduction, so it cannot wait for the float32 sum.
-constexpr int kGradWaves = 4, kGradNT = 4, kGradRows = 32;
-constexpr int kSlabLd = kGradRows + 8;  // 16-bit elements per column: 80 bytes keep 16-byte reads aligned
+// row.  The eight waves of a block decode a step of 64 rows by 128 columns
+// together (half a row tile each), multiply by the scales and store it row by
+// row in LDS; transposing reads (ds_read_b64_tr_b16: a lane receives one
+// column of four rows) then give the operands, for 64 columns by 16 NTW
+// tokens a wave.  Everything a step needs from memory, the tokens' rows of g
+// and the tiles' codes, codebooks and scales, comes by direct loads to LDS
+// whose lanes take consecutive addresses, one step ahead of its decoding.
+//
+// Scaled weights are rounded to the 16-bit type before the product: the scale
+// varies along the reduction, so it cannot wait for the float32 sum.
+//
+// Few tokens: the rows are split over blockIdx.z and the float32 partial sums
+// added in order by k_codes_grad_join.
+constexpr int kGradWaves = 8, kGradRows = 64;
 
-template <typename T, int GS>
+// 16-byte chunk of row m that holds columns 8 c .. 8 c + 7.  The 16 rows that
+// store the same chunk land on 16 distinct ones, and the eight rows that half
+// a wave reads (m % 16 in 0-3, 8-11 or in 4-7, 12-15), two chunks each, on
+// distinct pairs: neither repeats a bank.
+__device__ __forceinline__ int slab_chunk(int c, int m) {
+    return c ^ (((m & 3) << 1) | ((m >> 3 & 1) << 3) | (m >> 2 & 1));
+}
+
+// What a step brings to LDS.  A token's 64 values are 8 chunks of 16 bytes,
+// XOR-swizzled by the token so that the 16 tokens of a B operand lie on
+// distinct banks.
+template <int TT>
+struct GradStage {
+    char g[TT * kGradRows * 2];
+    char codes[kGradRows / 16 * kCodeTile];
+    char book[kGradRows * 32];
+    uint32_t scale[4][kGradRows];
+};
+
+// DIRECT: rows of g and codebooks start at 16-byte boundaries; otherwise they
+// are copied through registers.
+template <typename T, int NTW, int GS, bool DIRECT>
 __global__ __launch_bounds__(64 * kGradWaves) void k_codes_grad(
     const uint16_t* __restrict__ g, int64_t S, const char* __restrict__ codes, const uint16_t* __restrict__ table,
     int64_t table_rows, const uint16_t* __restrict__ scales, int64_t group, int64_t groups, int E, int64_t M,
-    int64_t K, int64_t MT, int64_t KT, const int32_t* __restrict__ offsets, uint16_t* __restrict__ out) {
+    int64_t K, int64_t MT, int64_t KT, const int32_t* __restrict__ offsets, int64_t steps_per, uint16_t* __restrict__ out,
+    float* __restrict__ part) {
     typedef Half<T> H;
-    constexpr int NT = kGradNT, TT = 16 * NT;
-    __shared__ __attribute__((aligned(16))) uint16_t s_slab[kGradWaves][kCodeCols * kSlabLd];
-    const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+    typedef short s16x4 __attribute__((ext_vector_type(4)));
+    constexpr int TT = kGradWaves / 2 * 16 * NTW, ROW = kCodeCols * 2, C = kCodeCols / 32, GROW = kGradRows * 2;
+    extern __shared__ __attribute__((aligned(16))) char s_mem[];
+    typedef GradStage<TT> Stage;
+    Stage* stage = (Stage*)s_mem;                       // [3]
+    auto slab = [&](int b) { return s_mem + 3 * sizeof(Stage) + b * (kGradRows * ROW); };
+    const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int r = lane & 15, q = lane >> 4;
     const Segment sg = find_segment(offsets, S, E, TT, blockIdx.y);
     if (sg.e < 0) return;
     const int64_t kt = blockIdx.x;
-    f32x4 acc[8][NT];
+    const int kh = w & 1, th = w >> 1;  // the wave's 64 columns and its 16 NTW tokens
+    f32x4 acc[C][NTW];
 #pragma unroll
-    for (int c = 0; c < 8; ++c)
+    for (int c = 0; c < C; ++c)
 #pragma unroll
-        for (int n = 0; n < NT; ++n) acc[c][n] = f32x4{0.f, 0.f, 0.f, 0.f};
-    uint16_t* slab = s_slab[w];
-    if (sg.e < E) {
-        const uint16_t* gr[NT];
+        for (int n = 0; n < NTW; ++n) acc[c][n] = f32x4{0.f, 0.f, 0.f, 0.f};
+    const int64_t all = (M + kGradRows - 1) / kGradRows;
+    const int64_t st0 = blockIdx.z * steps_per, st1 = st0 + steps_per < all ? st0 + steps_per : all;
+    if (sg.e < E && st0 < st1) {
+        const char* gb = (const char*)(g + sg.p0 * M);
+        const char* tab = (const char*)(table + (int64_t)sg.e * table_rows * 16);
+        const char* ct = codes + ((int64_t)sg.e * MT * KT + kt) * kCodeTile;
+        const char* sc = GS ? (const char*)(scales + (int64_t)sg.e * M * groups) : nullptr;
+        // step st to a stage: NTW + 2 direct loads a wave
+        auto fill = [&](int64_t st, Stage& to) {
+            const int64_t m0 = st * kGradRows;
+            const bool whole = m0 + kGradRows <= M;
+            if (DIRECT && whole) {
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
-            const int t = n * 16 + r < sg.n ? n * 16 + r : sg.n - 1;
-            gr[n] = g + (sg.p0 + t) * M + q * 8;
-        }
-        const uint16_t* tab = table + (int64_t)sg.e * table_rows * 16;
-        for (int64_t m0 = w * kGradRows; m0 < MT * 16; m0 += kGradWaves * kGradRows) {
-            u32x4 gv[NT];
-            const int64_t left = M - m0;
-#pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                int have = left >= kGradRows ? 8 : (int)left - q * 8;
-                gv[n] = load8(gr[n] + m0, have < 0 ? 0 : have);
-            }
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int64_t m = m0 + h * 16 + r;
-                const bool row = m < M;
-                const int64_t mc = row ? m : M - 1;
-                const Book book = load_book(tab, table_rows, mc);
-                u32x4 cw = u32x4{0, 0, 0, 0};
-                if (m0 / 16 + h < MT)
-                    cw = *(const u32x4*)(codes + (((int64_t)sg.e * MT + m0 / 16 + h) * KT + kt) * kCodeTile + lane * 16);
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    u32x4 a = decode8(book, cw[j]);
-                    float sv = 1.f;
-                    if (GS) {
-                        int64_t gi = GS == 1 ? kt * kCodeCols / group : kt * GS + j * GS / 4;
-                        if (gi >= groups) gi = groups - 1;
-                        sv = H::f32(scales[((int64_t)sg.e * M + mc) * groups + gi]);
-                    }
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        uint16_t v = (uint16_t)(a[e / 2] >> (16 * (e & 1)));
-                        if (GS) v = H::from(sv * H::f32(v));
-                        slab[(j * 32 + q * 8 + e) * kSlabLd + h * 16 + r] = row ? v : (uint16_t)0;
-                    }
+                for (int i = 0; i < NTW; ++i) {
+                    const int t0 = (i * kGradWaves + w) * 8, t = t0 + (lane >> 3);
+                    const int64_t src = t < sg.n ? t : sg.n - 1;
+                    dma16(gb, (uint32_t)(src * M * 2 + m0 * 2 + ((lane & 7) ^ (t >> 1 & 7)) * 16), to.g + t0 * GROW);
+                }
+            } else {
+                for (int i = threadIdx.x; i < TT * 8; i += 64 * kGradWaves) {
+                    const int t = i >> 3, c = i & 7;
+                    const int64_t src = t < sg.n ? t : sg.n - 1;
+                    const uint16_t* p = (const uint16_t*)gb + src * M + m0 + c * 8;
+                    *(u32x4*)(to.g + t * GROW + (c ^ (t >> 1 & 7)) * 16) =
+                        whole ? load8(p) : load8_end(p, (int)(M - m0) - c * 8);
                 }
             }
-            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-            __builtin_amdgcn_wave_barrier();
-#pragma unroll
-            for (int c = 0; c < 8; ++c) {
-                const u32x4 a = *(const u32x4*)(slab + (c * 16 + r) * kSlabLd + q * 8);
-#pragma unroll
-                for (int n = 0; n < NT; ++n) acc[c][n] = H::mfma(a, gv[n], acc[c][n]);
+            // slots 0-3: codes of a row tile; 4, 5: 32 codebooks; 6 + h: scales; the rest repeat slot 0
+            auto codes_of = [&](int i) {
+                const int64_t mt = st * (kGradRows / 16) + i;
+                dma16(ct, (uint32_t)((mt < MT ? mt : MT - 1) * KT * kCodeTile + lane * 16), to.codes + i * kCodeTile);
+            };
+            if (w < 4) {
+                codes_of(w);
+            } else if (w < 6) {
+                const int row = (w - 4) * 32 + (lane >> 1);
+                const int64_t m = m0 + row < M ? m0 + row : M - 1;
+                const uint32_t off = (uint32_t)((table_rows == 1 ? 0 : m) * 32 + (lane & 1) * 16);
+                if (DIRECT) dma16(tab, off, to.book + (w - 4) * 1024);
+                else *(u32x4*)(to.book + (w - 4) * 1024 + lane * 16) = *(const u32x4_any*)(tab + off);
             }
-            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-            __builtin_amdgcn_wave_barrier();
+            const int h = w >= 6 ? w - 6 : w;  // waves 6, 7: groups 0, 1; waves 2, 3: groups 2, 3
+            if (GS && (w >= 6 || (GS == 4 && (w == 2 || w == 3))) && h < GS) {
+                int64_t gi = GS == 1 ? kt * kCodeCols / group : kt * GS + h;
+                if (gi >= groups) gi = groups - 1;
+                const int64_t m = m0 + lane < M ? m0 + lane : M - 1;
+                dma2(sc, (uint32_t)((m * groups + gi) * 2), to.scale[h]);
+            }
+        };
+        // the wave's half of a row tile of step st, decoded and scaled, to a slab
+        auto decode = [&](int64_t st, const Stage& from, char* to) {
+            const int row = (w >> 1) * 16 + r;
+            const uint2 cw = *(const uint2*)(from.codes + (w >> 1) * kCodeTile + lane * 16 + (w & 1) * 8);
+            const u32x4* bk = (const u32x4*)(from.book + row * 32);
+            const Book book = make_book(bk[0], bk[1]);
+            const bool there = st * kGradRows + row < M;
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const int jj = (w & 1) * 2 + j;
+                const uint32_t c = j ? cw.y : cw.x;
+                u32x4 a = GS ? H::decode_scaled(book, c, (uint16_t)from.scale[jj * GS / 4][row]) : decode8(book, c);
+                if (!there) a = u32x4{0, 0, 0, 0};
+                *(u32x4*)(to + row * ROW + slab_chunk(jj * 4 + q, r) * 16) = a;
+            }
+        };
+        auto multiply = [&](const char* w16, const Stage& from) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                u32x4 gv[NTW];
+#pragma unroll
+                for (int n = 0; n < NTW; ++n) {
+                    const int t = (th * NTW + n) * 16 + r;
+                    gv[n] = *(const u32x4*)(from.g + t * GROW + ((h * 4 + q) ^ (t >> 1 & 7)) * 16);
+                }
+#pragma unroll
+                for (int c = 0; c < C; ++c) {
+                    // lane (r, q) wants column c * 16 + r of rows h * 32 + q * 8 .. + 8; it
+                    // fetches 8 bytes of row r / 4 (+ 4) of those, columns (r % 4) * 4 ..
+                    uint32_t a[4];
+#pragma unroll
+                    for (int f = 0; f < 2; ++f) {
+                        const int row = q * 8 + f * 4 + (r >> 2), col = kh * 64 + c * 16 + (r & 3) * 4;
+                        const char* at = w16 + (h * 32 + row) * ROW + slab_chunk(col >> 3, row & 15) * 16 + (col & 4) * 2;
+                        const s16x4 t = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                            (__attribute__((address_space(3))) s16x4*)at);
+                        a[2 * f] = __builtin_bit_cast(uint2, t).x;
+                        a[2 * f + 1] = __builtin_bit_cast(uint2, t).y;
+                    }
+#pragma unroll
+                    for (int n = 0; n < NTW; ++n)
+                        acc[c][n] = H::mfma(u32x4{a[0], a[1], a[2], a[3]}, gv[n], acc[c][n]);
+                }
+            }
+        };
+        auto landed = [&]() {  // every load of this wave is in LDS, then every wave's
+            __builtin_amdgcn_s_waitcnt(vmcnt_imm(0));
+            __syncthreads();
+        };
+        fill(st0, stage[0]);
+        landed();
+        if (st0 + 1 < st1) fill(st0 + 1, stage[1]);
+        decode(st0, stage[0], slab(0));
+        landed();
+        int cur = 0, nxt = 1, far = 2, buf = 0;
+        for (int64_t st = st0; st < st1; ++st) {
+            // here slab `buf` holds step st and stage `nxt` step st + 1
+            if (st + 2 < st1) fill(st + 2, stage[far]);
+            if (st + 1 < st1) decode(st + 1, stage[nxt], slab(buf ^ 1));
+            multiply(slab(buf), stage[cur]);
+            landed();
+            const int t = cur;
+            cur = nxt;
+            nxt = far;
+            far = t;
+            buf ^= 1;
         }
     }
-    // add the waves' sums in wave order, 16 columns at a time
-    f32x4* s_part = (f32x4*)&s_slab[0][0];  // [kGradWaves][NT][64]
 #pragma unroll
-    for (int c = 0; c < 8; ++c) {
-        __syncthreads();
+    for (int c = 0; c < C; ++c) {
+        const int64_t k = kt * kCodeCols + kh * 64 + c * 16 + q * 4;
+        if (k >= K) continue;
 #pragma unroll
-        for (int n = 0; n < NT; ++n) s_part[(w * NT + n) * 64 + lane] = acc[c][n];
-        __syncthreads();
-        const int n = w, l = lane;  // NT == kGradWaves: a wave per token tile
-        f32x4 v = s_part[n * 64 + l];
+        for (int n = 0; n < NTW; ++n) {
+            const int t = (th * NTW + n) * 16 + r;
+            if (t >= sg.n) continue;
+            const int64_t at = (sg.p0 + t) * K + k;
+            if (part) {
 #pragma unroll
-        for (int o = 1; o < kGradWaves; ++o) v += s_part[(o * NT + n) * 64 + l];
-        const int t = n * 16 + r;
-        const int64_t k = kt * kCodeCols + c * 16 + q * 4;
-        if (t < sg.n) {
-            uint16_t* to = out + (sg.p0 + t) * K + k;
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                if (k + e < K) to[e] = H::from(v[e]);
+                for (int e = 0; e < 4; ++e)
+                    if (k + e < K) part[blockIdx.z * S * K + at + e] = acc[c][n][e];
+            } else {
+                store4<T>(out + at, K - k, acc[c][n]);
+            }
         }
     }
 }
-static_assert(kGradNT == kGradWaves, "the epilogue gives each wave a token tile");
-static_assert(sizeof(f32x4) * kGradWaves * kGradNT * 64 <= sizeof(uint16_t) * kGradWaves * kCodeCols * kSlabLd,
-              "the partial sums reuse the slabs");
 
-size_t codes_product_grad_scratch(int64_t, int64_t, int64_t, int64_t) { return 0; }
+// out[i] = the sum of nsplit partial sums, in order.
+template <typename T>
+__global__ __launch_bounds__(256) void k_codes_grad_join(const float* __restrict__ part, int64_t n, int nsplit,
+                                                         uint16_t* __restrict__ out) {
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (i >= n) return;
+    float a = part[i];
+    for (int s = 1; s < nsplit; ++s) a += part[s * n + i];
+    out[i] = Half<T>::from(a);
+}
+
+// Splits of the rows: enough blocks for the device, at least four steps each.
+static bool grad_few(int64_t S, int64_t E) { return S <= 32 * E; }
+static int64_t grad_splits(int64_t S, int64_t E, int64_t M, int64_t K) {
+    const int64_t tt = grad_few(S, E) ? 64 : 256;
+    const int64_t blocks = code_tiles_k(K) * ((S < E ? S : E) + S / tt), steps = (M + kGradRows - 1) / kGradRows;
+    int64_t n = blocks > 0 ? 256 / blocks : 1;
+    if (n > steps / 4) n = steps / 4;
+    return n < 1 ? 1 : n > 64 ? 64 : n;
+}
+
+size_t codes_product_grad_scratch(int64_t S, int64_t E, int64_t M, int64_t K) {
+    const int64_t n = grad_splits(S, E, M, K);
+    return n > 1 ? ((size_t)(n * S * K) * sizeof(float) + 255) & ~(size_t)255 : 0;
+}
 
 template <typename T>
-static hipError_t grad_launch(const CodesArgs& a, hipStream_t s) {
+static hipError_t grad_launch(const CodesArgs& a, void* ws, hipStream_t s) {
     const int64_t MT = code_tiles_m(a.M), KT = code_tiles_k(a.K);
     const int64_t groups = a.scales ? (a.K + a.group - 1) / a.group : 0;
-#define KM_GO(GS)                                                                                                    \
-    hipLaunchKernelGGL((k_codes_grad<T, GS>),                                                                        \
-                       dim3((unsigned)KT, (unsigned)segment_tiles(a.S, a.E, a.offsets, 16 * kGradNT)),               \
-                       dim3(64 * kGradWaves), 0, s, (const uint16_t*)a.x, a.S, (const char*)a.codes,                 \
-                       (const uint16_t*)a.table, a.table_rows, (const uint16_t*)a.scales, a.group, groups, (int)a.E, \
-                       a.M, a.K, MT, KT, a.offsets, (uint16_t*)a.out)
+    const int64_t nsplit = grad_splits(a.S, a.E, a.M, a.K), steps = (a.M + kGradRows - 1) / kGradRows;
+    const int64_t per = (steps + nsplit - 1) / nsplit;
+    float* part = nsplit > 1 ? (float*)ws : nullptr;
+    const bool direct = a.M % 8 == 0 && (uintptr_t)a.x % 16 == 0 && (uintptr_t)a.table % 16 == 0;
+    hipError_t e = hipSuccess;
+#define KM_GO2(NTW, GS, DIR)                                                                                         \
+    do {                                                                                                             \
+        constexpr int TT = kGradWaves / 2 * 16 * NTW;                                                                \
+        const size_t lds = 3 * sizeof(GradStage<TT>) + 2 * kGradRows * kCodeCols * 2;                                \
+        if ((e = hipFuncSetAttribute((const void*)k_codes_grad<T, NTW, GS, DIR>,                                     \
+                                     hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds)) != hipSuccess)           \
+            return e;                                                                                                \
+        hipLaunchKernelGGL((k_codes_grad<T, NTW, GS, DIR>),                                                          \
+                           dim3((unsigned)KT, (unsigned)segment_tiles(a.S, a.E, a.offsets, TT), (unsigned)nsplit),   \
+                           dim3(64 * kGradWaves), lds, s, (const uint16_t*)a.x, a.S, (const char*)a.codes,           \
+                           (const uint16_t*)a.table, a.table_rows, (const uint16_t*)a.scales, a.group, groups,       \
+                           (int)a.E, a.M, a.K, MT, KT, a.offsets, per, (uint16_t*)a.out, part);                      \
+    } while (0)
+#define KM_GO(NTW, GS)                       \
+    do {                                     \
+        if (direct) KM_GO2(NTW, GS, true);   \
+        else KM_GO2(NTW, GS, false);         \
+    } while (0)
+#define KM_NT(GS)                              \
+    do {                                       \
+        if (grad_few(a.S, a.E)) KM_GO(1, GS);  \
+        else KM_GO(4, GS);                     \
+    } while (0)
     switch (groups_per_tile(a)) {
-        case 0: KM_GO(0); break;
-        case 1: KM_GO(1); break;
-        case 2: KM_GO(2); break;
-        default: KM_GO(4); break;
+        case 0: KM_NT(0); break;
+        case 1: KM_NT(1); break;
+        case 2: KM_NT(2); break;
+        default: KM_NT(4); break;
     }
+#undef KM_NT
 #undef KM_GO
+#undef KM_GO2
+    e = hipGetLastError();
+    if (e != hipSuccess || nsplit < 2) return e;
+    const int64_t n = a.S * a.K;
+    hipLaunchKernelGGL((k_codes_grad_join<T>), dim3((unsigned)((n + 255) / 256)), dim3(256), 0, s, part, n,
+                       (int)nsplit, (uint16_t*)a.out);
     return hipGetLastError();
 }
 
-hipError_t launch_codes_product_grad(DType xt, const CodesArgs& a, void*, hipStream_t s) {
+hipError_t launch_codes_product_grad(DType xt, const CodesArgs& a, void* ws, hipStream_t s) {
     if (a.S == 0 || a.K == 0) return hipSuccess;
-    return xt == DType::F16 ? grad_launch<_Float16>(a, s) : grad_launch<__bf16>(a, s);
+    return xt == DType::F16 ? grad_launch<_Float16>(a, ws, s) : grad_launch<__bf16>(a, ws, s);
 }
 
 }  // namespace km

@@ -65,6 +65,33 @@ __device__ __forceinline__ uint16_t f32_to_bf16_rne(float f) {
     return (uint16_t)(u >> 16);
 }
 
+constexpr uint32_t vmcnt_imm(int n) {  // s_waitcnt with only vmcnt <= n
+    return (uint32_t)((n & 15) | ((n >> 4) << 14) | (7 << 4) | (15 << 8));
+}
+
+// One global_load_lds_dwordx4: lane l copies 16 bytes from sbase + voff to
+// LDS byte lds + 16 l (sbase and lds are wave-uniform: an SGPR pair and M0).
+// Written as a one-instruction asm statement so the compiler does not treat
+// the in-flight LDS write as aliasing every later LDS read (it would wait for
+// the copy right after issuing it); the kernel waits on vmcnt explicitly
+// before the barrier that publishes a tile.  The instruction has no register
+// results.
+__device__ __forceinline__ void dma16(const char* sbase, uint32_t voff, const void* lds) {
+    const uint32_t l = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) void*)lds;
+    asm volatile("global_load_lds_dwordx4 %0, %1" ::"v"(voff), "s"(sbase),
+                 "{m0}"(__builtin_amdgcn_readfirstlane(l))
+                 : "memory");
+}
+
+// The same for 16-bit values: lane l copies 2 bytes to the low half of LDS
+// word lds + 4 l (the high half becomes zero).
+__device__ __forceinline__ void dma2(const char* sbase, uint32_t voff, const void* lds) {
+    const uint32_t l = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) void*)lds;
+    asm volatile("global_load_lds_ushort %0, %1" ::"v"(voff), "s"(sbase),
+                 "{m0}"(__builtin_amdgcn_readfirstlane(l))
+                 : "memory");
+}
+
 // Lanes of the wave whose v equals this lane's (among the lanes where
 // `active` holds): one ballot per bit of the values (0 <= v < 2^nbits).
 __device__ __forceinline__ uint64_t lanes_matching(int32_t v, int nbits, bool active) {
