@@ -102,106 +102,191 @@ __device__ __forceinline__ void store4(uint16_t* __restrict__ to, int64_t n, f32
 // A operand.  Lane (r, q) of a tile (r < 16 row, q < 4) holds 16 bytes of
 // codes, the four words of its row's 32-column steps j, whose eight columns
 // q * 8 .. are exactly the eight values it supplies to step j: no exchange
-// between lanes.  A block takes one row tile and TT = 16 NT tokens; its waves
-// split the columns (tile w, w + W, ...) and add their sums in LDS in wave
-// order.  Scales multiply the float32 sum of their group (GS groups in a
-// tile), so weights are never rounded after the codebook.
-constexpr int kProdWaves = 8;
+// between lanes.  Scales multiply the float32 sum of their group (GS groups
+// in a tile), so weights are never rounded after the codebook.
+//
+// A block takes WR row tiles and 16 NT tokens, a wave one row tile and one of
+// WK parts of the columns; the columns go by in chunks of WK * U tiles, of
+// which a wave has U, all requested a chunk ahead.  With a row tile for every
+// wave (WK = 1) the tokens are read once for WR tiles and no sums are
+// exchanged; WK > 1 makes more waves where there are few row tiles, and the
+// parts are added in LDS in their order.
+//
+// XLDS: a chunk's tokens come to LDS by direct loads of whole lines (their
+// operand layout, 16 bytes from each of 16 rows, would cost a cache look-up
+// per lane), 16-byte chunks XOR-swizzled by the token against bank conflicts.
+// Otherwise (one token, whose loads are broadcasts, or rows without 16-byte
+// alignment) operands are loaded as they are.
+template <int WR, int WK, int U, int NT, int GS, bool XLDS>
+struct ProductLds {
+    static constexpr int TILE = 16 * NT * kCodeCols * 2;            // x of one tile
+    static constexpr int X = XLDS ? 2 * WK * U * TILE : 0;          // two chunks
+    static constexpr int SCALE = GS * 4 * 16 * 4;                   // a wave's scales: [4][GS][16]
+    static constexpr int SUMS = WK > 1 ? WR * WK * NT * 64 * 16 : 0;
+    static constexpr int LOOP = X + WR * WK * SCALE;
+    static constexpr int BYTES = LOOP > SUMS ? LOOP : SUMS;
+};
 
-template <typename T, int NT, int GS>
-__global__ __launch_bounds__(64 * kProdWaves) void k_codes_product(
+template <typename T, int WR, int WK, int U, int NT, int GS, bool XLDS>
+__global__ __launch_bounds__(64 * WR * WK) void k_codes_product(
     const uint16_t* __restrict__ x, int64_t S, const char* __restrict__ codes, const uint16_t* __restrict__ table,
     int64_t table_rows, const uint16_t* __restrict__ scales, int64_t group, int64_t groups, int E, int64_t M,
     int64_t K, int64_t MT, int64_t KT, const int32_t* __restrict__ offsets, uint16_t* __restrict__ out) {
     typedef Half<T> H;
-    __shared__ f32x4 s_acc[kProdWaves][NT][64];
-    const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
-    const int r = lane & 15, q = lane >> 4;
-    const Segment g = find_segment(offsets, S, E, 16 * NT, blockIdx.y);
+    typedef ProductLds<WR, WK, U, NT, GS, XLDS> L;
+    constexpr int TT = 16 * NT, ROW = kCodeCols * 2, NG = GS ? GS : 1, W = WR * WK, CH = WK * U;
+    static_assert(U <= 4, "a quarter of the lanes loads a tile's scales");
+    extern __shared__ __attribute__((aligned(16))) char s_mem[];  // x, scales; then the sums
+    const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wr = w / WK, wk = w % WK, r = lane & 15, q = lane >> 4;
+    float* s_scale = (float*)(s_mem + L::X + w * L::SCALE);  // [4][NG][16]
+    const Segment g = find_segment(offsets, S, E, TT, blockIdx.y);
     if (g.e < 0) return;
-    const int64_t mt = blockIdx.x;
-    const bool zero = g.e == E;  // rows past the last expert's
+    const int64_t mt = (int64_t)blockIdx.x * WR + wr;
     f32x4 acc[NT];
 #pragma unroll
     for (int n = 0; n < NT; ++n) acc[n] = f32x4{0.f, 0.f, 0.f, 0.f};
-    if (!zero) {
-        const char* cm = codes + ((int64_t)g.e * MT + mt) * KT * kCodeTile + lane * 16;
+    if (g.e < E) {  // (expert E stands for the rows past the last expert's)
+        const int64_t whole = K / kCodeCols, mc = mt < MT ? mt : MT - 1, mrow = mc * 16 + r < M ? mc * 16 + r : M - 1;
+        const char* xs = (const char*)(x + g.p0 * K);
+        const char* cm = codes + ((int64_t)g.e * MT + mc) * KT * kCodeTile + lane * 16;
         const uint16_t* xr[NT];
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
             const int t = n * 16 + r < g.n ? n * 16 + r : g.n - 1;  // absent tokens read the last one
-            xr[n] = x + (g.p0 + t) * K + q * 8;
+            xr[n] = (const uint16_t*)xs + (int64_t)t * K + q * 8;
         }
-        const uint16_t* sc[4];
-        if (GS) {
+        const uint16_t* srow = GS ? scales + ((int64_t)g.e * M + mrow) * groups : nullptr;
+        // a wave's part of a chunk: U tiles of codes; lane (r, q): the scales of row r, tile q
+        struct Part {
+            u32x4 cw[U];
+            uint16_t sc[NG];
+        };
+        auto fetch = [&](int64_t c0, Part& p) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int64_t m = mt * 16 + q * 4 + i < M ? mt * 16 + q * 4 + i : M - 1;
-                sc[i] = scales + ((int64_t)g.e * M + m) * groups;
+            for (int u = 0; u < U; ++u) {
+                const int64_t kt = c0 + u * WK + wk;
+                p.cw[u] = *(const u32x4*)(cm + (kt < KT ? kt : KT - 1) * kCodeTile);
             }
-        }
-        const int64_t mr = mt * 16 + r < M ? mt * 16 + r : M - 1;
-        const Book book = load_book(table + (int64_t)g.e * table_rows * 16, table_rows, mr);
-        // one tile; END: the last one of a row that is no multiple of 128 columns, of which `left` are there
-        auto tile = [&](int64_t kt, auto end_tag, int left) {
-            constexpr bool END = decltype(end_tag)::value;
-            const u32x4 cw = *(const u32x4*)(cm + kt * kCodeTile);
-            u32x4 xv[NT][4];
-#pragma unroll
-            for (int n = 0; n < NT; ++n)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const uint16_t* p = xr[n] + kt * kCodeCols + j * 32;
-                    xv[n][j] = END ? load8_end(p, left - j * 32 - q * 8) : load8(p);
-                }
-            float sv[4][GS ? GS : 1];
             if (GS) {
+                const int64_t kt = c0 + (U < 4 ? q % U : q) * WK + wk;
 #pragma unroll
-                for (int h = 0; h < GS; ++h) {
-                    int64_t gi = GS == 4 ? kt * 4 + h : GS == 2 ? kt * 2 + h : kt * kCodeCols / group;
+                for (int h = 0; h < NG; ++h) {
+                    int64_t gi = GS == 1 ? kt * kCodeCols / group : kt * GS + h;
                     if (gi >= groups) gi = groups - 1;
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) sv[i][h] = H::f32(sc[i][gi]);
+                    p.sc[h] = srow[gi];
                 }
             }
+        };
+        // the block's x of a chunk, in instructions of 1 KB: 4 tokens by 128 columns
+        auto fill = [&](int64_t c0, int buf) {
+            constexpr int NI = CH * TT / 4;
+#pragma unroll
+            for (int i = 0; i < (NI + W - 1) / W; ++i) {
+                const int id = i * W + w, ti = id / (TT / 4), tk = id % (TT / 4) * 4 + (lane >> 4);
+                const int64_t kt = c0 + ti;
+                if (id < NI && kt < whole) {
+                    const int64_t src = tk < g.n ? tk : g.n - 1;
+                    dma16(xs, (uint32_t)(src * K * 2 + kt * ROW + ((lane & 15) ^ (tk & 15)) * 16),
+                          s_mem + buf * CH * L::TILE + id * 1024);
+                }
+            }
+        };
+        const Book book = load_book(table + (int64_t)g.e * table_rows * 16, table_rows, mrow);
+        // tile kt from its codes and x; `at` is its place among the wave's scales.
+        // END: the last tile of a row that is no multiple of 128 columns.
+        auto multiply = [&](int64_t kt, u32x4 cw, int at, const char* xl, auto end_tag) {
+            constexpr bool END = decltype(end_tag)::value;
+            const int left = (int)(K - kt * kCodeCols);
             f32x4 part[NT];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                u32x4 a = decode8(book, cw[j]);
+                u32x4 xv[NT];
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    const uint16_t* p = xr[n] + kt * kCodeCols + j * 32;
+                    if constexpr (END) xv[n] = load8_end(p, left - j * 32 - q * 8);
+                    else if constexpr (XLDS) xv[n] = *(const u32x4*)(xl + (n * 16 + r) * ROW + ((j * 4 + q) ^ r) * 16);
+                    else xv[n] = load8(p);
+                }
+                const bool start = GS && j % (4 / NG) == 0, end = GS && (j + 1) % (4 / NG) == 0;
+                u32x4 av = decode8(book, cw[j]);
                 // columns past the row's end: x is zero there, and so must the weight be (0 * inf is no zero)
-                if (END) a = keep8(a, left - j * 32 - q * 8);
-                const bool start = GS && j % (4 / (GS ? GS : 1)) == 0;
-                const bool end = GS && (j + 1) % (4 / (GS ? GS : 1)) == 0;
+                if (END) av = keep8(av, left - j * 32 - q * 8);
+                f32x4 sv;
+                if (end) sv = *(const f32x4*)&s_scale[(at * NG + j * NG / 4) * 16 + q * 4];
 #pragma unroll
                 for (int n = 0; n < NT; ++n) {
                     if (!GS) {
-                        acc[n] = H::mfma(a, xv[n][j], acc[n]);
+                        acc[n] = H::mfma(av, xv[n], acc[n]);
                     } else {
-                        part[n] = H::mfma(a, xv[n][j], start ? f32x4{0.f, 0.f, 0.f, 0.f} : part[n]);
+                        part[n] = H::mfma(av, xv[n], start ? f32x4{0.f, 0.f, 0.f, 0.f} : part[n]);
                         if (end) {
 #pragma unroll
-                            for (int i = 0; i < 4; ++i)
-                                acc[n][i] = fmaf(sv[i][j * (GS ? GS : 1) / 4], part[n][i], acc[n][i]);
+                            for (int i = 0; i < 4; ++i) acc[n][i] = fmaf(sv[i], part[n][i], acc[n][i]);
                         }
                     }
                 }
             }
         };
-        const int64_t whole = K / kCodeCols;
-        for (int64_t kt = w; kt < whole; kt += kProdWaves) tile(kt, Tag<false>{}, 0);
-        if (whole < KT && whole % kProdWaves == w) tile(whole, Tag<true>{}, (int)(K - whole * kCodeCols));
+        auto keep_scales = [&](const Part& p) {
+            if (GS) {
+#pragma unroll
+                for (int h = 0; h < NG; ++h) s_scale[(q * NG + h) * 16 + r] = H::f32(p.sc[h]);
+            }
+        };
+        Part p[2];
+        fetch(0, p[0]);
+        if (XLDS) fill(0, 0);
+        for (int64_t c0 = 0; c0 < whole; c0 += 2 * CH) {
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+                const int64_t c = c0 + b * CH;
+                if (c >= whole) break;  // (block-uniform)
+                if (XLDS) {
+                    __builtin_amdgcn_s_waitcnt(vmcnt_imm(0));  // this wave's direct loads, then everybody's
+                    __syncthreads();
+                }
+                if (c + CH < whole) {
+                    fetch(c + CH, p[b ^ 1]);
+                    if (XLDS) fill(c + CH, b ^ 1);
+                }
+                keep_scales(p[b]);
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    const int64_t kt = c + u * WK + wk;
+                    if (kt < whole)
+                        multiply(kt, p[b].cw[u], u, s_mem + (b * CH + u * WK + wk) * L::TILE, Tag<false>{});
+                }
+            }
+        }
+        if (whole < KT && whole % WK == wk) {
+            fetch(whole - wk, p[0]);
+            keep_scales(p[0]);
+            multiply(whole, p[0].cw[0], 0, nullptr, Tag<true>{});
+        }
     }
+    auto store = [&](int n, int64_t tile, int l, f32x4 v) {
+        const int tk = n * 16 + (l & 15);
+        const int64_t m = tile * 16 + (l >> 4) * 4;
+        if (tk < g.n && m < M) store4<T>(out + (g.p0 + tk) * M + m, M - m, v);
+    };
+    if constexpr (WK == 1) {
 #pragma unroll
-    for (int n = 0; n < NT; ++n) s_acc[w][n][lane] = acc[n];
-    __syncthreads();
-    for (int i = threadIdx.x; i < NT * 64; i += 64 * kProdWaves) {
-        const int n = i >> 6, l = i & 63;
-        f32x4 v = s_acc[0][n][l];
+        for (int n = 0; n < NT; ++n) store(n, mt, lane, acc[n]);
+    } else {
+        __syncthreads();  // x and scales become the waves' sums
+        f32x4* sums = (f32x4*)s_mem;  // [WR][WK][NT][64]
 #pragma unroll
-        for (int o = 1; o < kProdWaves; ++o) v += s_acc[o][n][l];
-        const int t = n * 16 + (l & 15);
-        const int64_t m = mt * 16 + (l >> 4) * 4;
-        if (t < g.n && m < M) store4<T>(out + (g.p0 + t) * M + m, M - m, v);
+        for (int n = 0; n < NT; ++n) sums[(w * NT + n) * 64 + lane] = acc[n];
+        __syncthreads();
+        for (int i = threadIdx.x; i < WR * NT * 64; i += 64 * W) {
+            const int a = i / (NT * 64), rest = i % (NT * 64);
+            f32x4 v = sums[a * WK * NT * 64 + rest];
+#pragma unroll
+            for (int o = 1; o < WK; ++o) v += sums[(a * WK + o) * NT * 64 + rest];
+            store(rest >> 6, (int64_t)blockIdx.x * WR + a, rest & 63, v);
+        }
     }
 }
 
@@ -213,6 +298,11 @@ __global__ __launch_bounds__(64 * kProdWaves) void k_codes_product(
 // NT rows of 128 columns, two buffers) comes to LDS by direct loads, its
 // 16-byte chunks XOR-swizzled by the row so that the 16 rows a B operand
 // reads lie on distinct banks.
+#ifndef PW
+#define PW 1
+#define PR 8
+#define PU 4
+#endif
 #ifndef GOCC
 #define GOCC 2
 #define GNT 6
@@ -392,36 +482,47 @@ template <typename T>
 static hipError_t product_launch(const CodesArgs& a, hipStream_t s) {
     const int64_t MT = code_tiles_m(a.M), KT = code_tiles_k(a.K);
     const int64_t groups = a.scales ? (a.K + a.group - 1) / a.group : 0;
-    const bool few = a.S <= 16 * a.E;
-    const bool many = a.S >= 64 * a.E && a.K % 8 == 0 && (uintptr_t)a.x % 16 == 0;
+    const bool aligned = a.K % 8 == 0 && (uintptr_t)a.x % 16 == 0;
+    const bool many = a.S >= 64 * a.E && aligned;
+    hipError_t e = hipSuccess;
+#define KM_ARGS                                                                                                      \
+    s, (const uint16_t*)a.x, a.S, (const char*)a.codes, (const uint16_t*)a.table, a.table_rows,                      \
+        (const uint16_t*)a.scales, a.group, groups, (int)a.E, a.M, a.K, MT, KT, a.offsets, (uint16_t*)a.out
 #define KM_MANY(GS)                                                                                                  \
-    hipLaunchKernelGGL((k_codes_gemm<T, kGemmNT, GS>),                                                                     \
+    hipLaunchKernelGGL((k_codes_gemm<T, kGemmNT, GS>),                                                               \
                        dim3((unsigned)((MT + kGemmWaves * kGemmR - 1) / (kGemmWaves * kGemmR)),                      \
-                            (unsigned)segment_tiles(a.S, a.E, a.offsets, 16 * kGemmNT)),                                    \
-                       dim3(64 * kGemmWaves), 0, s, (const uint16_t*)a.x, a.S, (const char*)a.codes,                 \
-                       (const uint16_t*)a.table, a.table_rows, (const uint16_t*)a.scales, a.group, groups, (int)a.E, \
-                       a.M, a.K, MT, KT, a.offsets, (uint16_t*)a.out)
-#define KM_GO(NT, GS)                                                                                                \
-    hipLaunchKernelGGL((k_codes_product<T, NT, GS>),                                                                 \
-                       dim3((unsigned)MT, (unsigned)segment_tiles(a.S, a.E, a.offsets, 16 * NT)),                    \
-                       dim3(64 * kProdWaves), 0, s, (const uint16_t*)a.x, a.S, (const char*)a.codes,                 \
-                       (const uint16_t*)a.table, a.table_rows, (const uint16_t*)a.scales, a.group, groups, (int)a.E, \
-                       a.M, a.K, MT, KT, a.offsets, (uint16_t*)a.out)
-#define KM_NT(GS)           \
-    do {                    \
-        if (few) KM_GO(1, GS); \
-        else if (many) KM_MANY(GS); \
-        else KM_GO(4, GS);  \
+                            (unsigned)segment_tiles(a.S, a.E, a.offsets, 16 * kGemmNT)),                             \
+                       dim3(64 * kGemmWaves), 0, KM_ARGS)
+#define KM_FEW(WR, WK, U, NT, GS, XLDS)                                                                              \
+    do {                                                                                                             \
+        constexpr size_t lds = ProductLds<WR, WK, U, NT, GS, XLDS>::BYTES;                                           \
+        if (lds > 64 * 1024 &&                                                                                       \
+            (e = hipFuncSetAttribute((const void*)k_codes_product<T, WR, WK, U, NT, GS, XLDS>,                       \
+                                     hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds)) != hipSuccess)           \
+            return e;                                                                                                \
+        hipLaunchKernelGGL((k_codes_product<T, WR, WK, U, NT, GS, XLDS>),                                            \
+                           dim3((unsigned)((MT + WR - 1) / WR), (unsigned)segment_tiles(a.S, a.E, a.offsets, 16 * NT)), \
+                           dim3(64 * WR * WK), lds, KM_ARGS);                                                        \
+    } while (0)
+    const int64_t row_tiles = MT * (a.S < a.E ? a.S : a.E);  // at most, over the experts
+#define KM_PICK(GS)                                                     \
+    do {                                                                \
+        if (many) KM_MANY(GS);                                          \
+        else if (a.S == 1 || !aligned) KM_FEW(1, 8, 4, 1, GS, false);   \
+        else if (row_tiles < 2048) KM_FEW(1, 8, 1, 1, GS, true);        \
+        else if (a.S > 16 * a.E) KM_FEW(PR, PW, PU, 2, GS, true);       \
+        else KM_FEW(PR, PW, PU, 1, GS, true);                           \
     } while (0)
     switch (groups_per_tile(a)) {
-        case 0: KM_NT(0); break;
-        case 1: KM_NT(1); break;
-        case 2: KM_NT(2); break;
-        default: KM_NT(4); break;
+        case 0: KM_PICK(0); break;
+        case 1: KM_PICK(1); break;
+        case 2: KM_PICK(2); break;
+        default: KM_PICK(4); break;
     }
-#undef KM_NT
+#undef KM_PICK
+#undef KM_FEW
 #undef KM_MANY
-#undef KM_GO
+#undef KM_ARGS
     return hipGetLastError();
 }
 
