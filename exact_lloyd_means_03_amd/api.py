@@ -42,7 +42,14 @@ def _points(x):
     return x.shape
 
 
+# The current stream's handle; building torch's Stream object for it takes
+# about as long as launching a kernel.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(dev):
+    if _raw_stream is not None and dev.index is not None:
+        return _raw_stream(dev.index)
     return torch.cuda.current_stream(dev).cuda_stream
 
 

@@ -360,8 +360,11 @@ struct KeySortPlan {
     size_t keys = 0, order = 0, keys2 = 0, order2 = 0, hist = 0, prefix = 0, counts = 0, total = 0;
 };
 KeySortPlan plan_key_sort(int64_t B, int64_t N, int64_t V);
+bool count_rank_fits(int64_t B, int64_t N);  // one launch ranks the labels
+// clear (only where count_rank_fits): B times clear_bytes bytes to set to zero
+// beside the ranking.
 hipError_t launch_key_sort(const int32_t* labels, int64_t B, int64_t N, int64_t V, const KeySortPlan& p, char* ws,
-                           hipStream_t s);
+                           hipStream_t s, void* clear = nullptr, int64_t clear_bytes = 0);
 
 // Rows by label (rows.hip).
 hipError_t launch_lookup(DType xt, const void* table, int64_t B, int64_t V, int64_t d, const int32_t* labels,

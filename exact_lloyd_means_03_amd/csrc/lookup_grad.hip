@@ -8,7 +8,7 @@
 // slice, summing in float32 registers; a label that begins and ends in the
 // piece is rounded and stored at once, so nothing but the gradient itself is
 // written for it.  Sums of labels that cross a piece's border go to the
-// piece's two float32 slots and are added in sorted order by a second launch.
+// piece's two float32 slots and are added in a fixed order by a second launch.
 // No float atomics: the result is a function of the inputs alone.
 //
 // HBM bound: every row read once, every table row written once.  Rows of
@@ -39,7 +39,7 @@ __device__ __forceinline__ int64_t wave_lower_bound(const int32_t* __restrict__ 
 // The group's piece: TW sorted rows from p * TW on, columns of chunk
 // slice * GL + (lane in group).  slot[b][p][0]: the part of a label that began
 // in an earlier piece; slot[b][p][1]: the part of one that goes on in the next.
-template <typename TI, typename TO, int GL>
+template <typename TI, typename TO, int GL, bool STREAM>
 __device__ __forceinline__ void reduce_piece(const TI* __restrict__ g, int64_t N, int d, int C,
                                              const int32_t* __restrict__ keys, const int32_t* __restrict__ order,
                                              int32_t V, int TW, int64_t p, int slice, int gl, float scale,
@@ -62,7 +62,7 @@ __device__ __forceinline__ void reduce_piece(const TI* __restrict__ g, int64_t N
         float a[VN];
 #pragma unroll
         for (int i = 0; i < VN; ++i) a[i] = scale * acc[i];
-        store_f32<TO, VN>(out + (int64_t)cur * d + e0, d, a);
+        store_f32<TO, VN, STREAM>(out + (int64_t)cur * d + e0, d, a);
     };
     for (int64_t q = q0; q < q1; q += U) {
         int32_t key[U], idx[U];
@@ -102,7 +102,7 @@ __device__ __forceinline__ void reduce_piece(const TI* __restrict__ g, int64_t N
 }
 
 // Clears the table rows [v0, v0 + RZ) that no label names.
-template <typename TO>
+template <typename TO, bool STREAM>
 __device__ __forceinline__ void clear_rows(const int32_t* __restrict__ keys, int64_t N, int64_t V, int d, int64_t v0,
                                            int RZ, int lane, TO* __restrict__ out) {
     if (v0 >= V) return;
@@ -128,13 +128,14 @@ __device__ __forceinline__ void clear_rows(const int32_t* __restrict__ keys, int
         const int len = rest ? __builtin_ctzll(rest) : 64 - r;
         TO* to = out + (v0 + r) * d;
         const int64_t n = (int64_t)len * d, nv = n / VN;
-        for (int64_t i = lane; i < nv; i += 64) *(typename RowVec<TO>::VU*)(to + i * VN) = typename RowVec<TO>::V{};
+        for (int64_t i = lane; i < nv; i += 64)
+            store_raw<TO, STREAM>(to + i * VN, VN, typename RowVec<TO>::V{});
         if (lane < n - nv * VN) to[nv * VN + lane] = TO{};
         empty &= len + r < 64 ? ~(uint64_t)0 << (len + r) : 0;
     }
 }
 
-template <typename TI, typename TO, int GL>
+template <typename TI, typename TO, int GL, bool STREAM>
 __global__ __launch_bounds__(kGradThreads) void k_lookup_grad(const TI* __restrict__ g, int64_t N, int d, int C,
                                                               const int32_t* __restrict__ keys,
                                                               const int32_t* __restrict__ order, int64_t V, int TW,
@@ -148,63 +149,117 @@ __global__ __launch_bounds__(kGradThreads) void k_lookup_grad(const TI* __restri
         const int64_t gid = ((int64_t)blockIdx.x * kGradThreads + threadIdx.x) / GL;
         const int64_t p = gid / slices;
         if (p >= npieces) return;
-        reduce_piece<TI, TO, GL>(g + b * N * d, N, d, C, keys, order + b * N, (int32_t)V, TW, p,
+        reduce_piece<TI, TO, GL, STREAM>(g + b * N * d, N, d, C, keys, order + b * N, (int32_t)V, TW, p,
                                  (int)(gid - p * slices), threadIdx.x % GL, scale, out,
                                  slot + b * npieces * 2 * (int64_t)d);
         return;
     }
     const int64_t wv = ((int64_t)blockIdx.x - red_blocks) * (kGradThreads / 64) + (threadIdx.x >> 6);
-    clear_rows<TO>(keys, N, V, d, wv * RZ, RZ, threadIdx.x & 63, out);
+    clear_rows<TO, STREAM>(keys, N, V, d, wv * RZ, RZ, threadIdx.x & 63, out);
 }
 
-// One block per (piece, column slice of 64 chunks): if a label begins in piece
-// p and goes on in p + 1, its row is slot[p][1] plus slot[q][0] of the pieces
-// q it reaches, in that order within each of the block's four waves' ranges of
-// pieces and over the waves.
-template <typename TI, typename TO>
-__global__ __launch_bounds__(kGradThreads) void k_lookup_grad_fold(const int32_t* __restrict__ keys, int64_t N, int d,
+// Labels that cross piece borders.  A label that begins in piece p and reaches
+// pieces p + 1 .. last has the row slot[p][1] + slot[p + 1][0] + .. +
+// slot[last][0].  Up to kFoldShort pieces are added in that order by a group
+// of GL lanes, one per (piece, column slice).  Longer runs are left to the
+// blocks behind those, one per (kFoldShort pieces, column slice): at most one
+// such run begins in them, the one that goes on past their end.  Its pieces are
+// split over the block's waves, added in order within a wave and over
+// the waves.
+constexpr int kFoldShort = 16, kFoldU = 8;
+// Wide rows have few slices a block could serve beside each other: big blocks.
+constexpr int fold_threads(int GL) { return GL == 64 ? 1024 : 256; }
+
+template <int VN>
+__device__ __forceinline__ void add_slot(float (&acc)[VN], const float* __restrict__ from, int d) {
+    if (d >= VN) {
+#pragma unroll
+        for (int i = 0; i < VN; ++i) acc[i] += from[i];
+    } else {
+        for (int i = 0; i < d; ++i) acc[i] += from[i];
+    }
+}
+
+// slot[q][0] of the pieces q in [a, z), kFoldU of them in flight.
+template <int VN>
+__device__ __forceinline__ void add_slots(float (&acc)[VN], const float* __restrict__ slot, int64_t a, int64_t z,
+                                          int e0, int d) {
+    int64_t q = a;
+    if (d >= VN) {
+        for (; q + kFoldU <= z; q += kFoldU) {
+            float v[kFoldU][VN];
+#pragma unroll
+            for (int u = 0; u < kFoldU; ++u)
+#pragma unroll
+                for (int i = 0; i < VN; ++i) v[u][i] = slot[(q + u) * 2 * (int64_t)d + e0 + i];
+#pragma unroll
+            for (int u = 0; u < kFoldU; ++u)
+#pragma unroll
+                for (int i = 0; i < VN; ++i) acc[i] += v[u][i];
+        }
+    }
+    for (; q < z; ++q) add_slot<VN>(acc, slot + q * 2 * (int64_t)d + e0, d);
+}
+
+template <typename TI, typename TO, int GL>
+__global__ __launch_bounds__(fold_threads(GL)) void k_lookup_grad_fold(const int32_t* __restrict__ keys, int64_t N, int d,
                                                                    int C, int64_t V, int TW, int64_t npieces,
-                                                                   int slices, float scale, TO* __restrict__ out,
+                                                                   int slices, int64_t short_blocks, int long_slices,
+                                                                   float scale, TO* __restrict__ out,
                                                                    const float* __restrict__ slot) {
-    constexpr int VN = RowVec<TI>::N, NW = kGradThreads / 64, U = 4;
+    constexpr int VN = RowVec<TI>::N, FT = fold_threads(GL), NW = FT / 64;
     __shared__ float s_acc[NW][64][VN + 1];
     const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
     const int64_t b = blockIdx.y;
-    const int64_t p = blockIdx.x / slices;
-    const int slice = (int)(blockIdx.x - p * slices);
     keys += b * N;
     slot += b * npieces * 2 * (int64_t)d;
     out += b * V * d;
-    const int64_t q0 = p * TW, q1 = q0 + TW;  // q1 <= N - 1 here: the launch has no block for the last piece
-    const int32_t v = keys[q1 - 1];
-    if (v >= V || keys[q1] != v) return;                 // nothing goes on
-    if (q0 > 0 && keys[q0 - 1] == v) return;             // it began earlier
-    const int64_t end = wave_lower_bound(keys + q1, N - q1, (int64_t)v + 1, lane) + q1;
-    const int64_t last = (end - 1) / TW;                 // the last piece it reaches
-    const int c = slice * 64 + lane;
-    const bool live = c < C;
-    const int e0 = live ? chunk_at<TI>(c, d) : 0;
-    const int64_t n = last - p, per = (n + NW - 1) / NW;  // pieces p + 1 .. last over the waves
-    const int64_t a = p + 1 + w * per, z = a + per < last + 1 ? a + per : last + 1;
     float acc[VN];
 #pragma unroll
     for (int i = 0; i < VN; ++i) acc[i] = 0.f;
-    auto add = [&](const float* from) {
-        if (d >= VN) {
+    if ((int64_t)blockIdx.x < short_blocks) {
+        const int64_t gid = ((int64_t)blockIdx.x * FT + threadIdx.x) / GL, p = gid / slices;
+        const int c = (int)(gid - p * slices) * GL + threadIdx.x % GL;
+        if (p + 1 >= npieces || c >= C) return;
+        const int64_t q0 = p * TW, q1 = q0 + TW;
+        const int32_t v = keys[q1 - 1];
+        if (v >= V || keys[q1] != v || (q0 > 0 && keys[q0 - 1] == v)) return;  // nothing begins here and goes on
+        // how many of the next kFoldShort + 1 pieces begin with v (the first ones, as keys are sorted)
+        int n = 0;
 #pragma unroll
-            for (int i = 0; i < VN; ++i) acc[i] += from[i];
-        } else {
-            for (int i = 0; i < d; ++i) acc[i] += from[i];
+        for (int i = 1; i <= kFoldShort + 1; ++i) {
+            const int64_t q = p + i < npieces ? p + i : npieces - 1;
+            n += p + i < npieces && keys[q * TW] == v;
         }
-    };
+        if (n > kFoldShort) return;
+        const int e0 = chunk_at<TI>(c, d);
+        add_slot<VN>(acc, slot + (p * 2 + 1) * (int64_t)d + e0, d);
+        add_slots<VN>(acc, slot, p + 1, p + 1 + n, e0, d);
+#pragma unroll
+        for (int i = 0; i < VN; ++i) acc[i] *= scale;
+        store_f32<TO, VN>(out + (int64_t)v * d + e0, d, acc);
+        return;
+    }
+    const int64_t id = (int64_t)blockIdx.x - short_blocks, grp = id / long_slices;
+    const int c = (int)(id - grp * long_slices) * 64 + lane;
+    const int64_t pe = (grp + 1) * kFoldShort;  // the first piece after the block's
+    if (pe >= npieces) return;
+    const int32_t v = keys[pe * TW];
+    if (v >= V || keys[pe * TW - 1] != v) return;
+    // lane i: does v come from before piece pe - 1 - i?  The first lane that says no is the piece it begins in
+    const int64_t back = pe - 1 - lane;
+    const uint64_t here = __ballot(lane < kFoldShort && (back == 0 || keys[back * TW - 1] != v));
+    if (!here) return;  // it begins before the block's pieces
+    const int64_t p = pe - 1 - __builtin_ctzll(here);
+    const int64_t q1 = pe * TW, end = q1 + wave_lower_bound(keys + q1, N - q1, (int64_t)v + 1, lane);
+    const int64_t last = (end - 1) / TW;
+    if (last - p <= kFoldShort) return;
+    const bool live = c < C;
+    const int e0 = live ? chunk_at<TI>(c, d) : 0;
+    const int64_t per = (last - p + NW - 1) / NW, a = p + 1 + w * per, z = a + per < last + 1 ? a + per : last + 1;
     if (live) {
-        if (w == 0) add(slot + (p * 2 + 1) * (int64_t)d + e0);
-        int64_t q = a;
-        for (; q + U <= z; q += U) {
-#pragma unroll
-            for (int u = 0; u < U; ++u) add(slot + (q + u) * 2 * (int64_t)d + e0);
-        }
-        for (; q < z; ++q) add(slot + q * 2 * (int64_t)d + e0);
+        if (w == 0) add_slot<VN>(acc, slot + (p * 2 + 1) * (int64_t)d + e0, d);
+        add_slots<VN>(acc, slot, a, z, e0, d);
     }
 #pragma unroll
     for (int i = 0; i < VN; ++i) s_acc[w][lane][i] = acc[i];
@@ -225,8 +280,8 @@ __global__ __launch_bounds__(kGradThreads) void k_lookup_grad_fold(const int32_t
 // waves.  At least 16 (a slot of 4 bytes an element costs an eighth of reading
 // 16 rows of 16-bit elements), doubled to 256 while 8192 waves remain.
 static int grad_tw(int64_t B, int64_t N, int64_t slices_waves64) {
-    int tw = 16;
-    while (tw < 256 && B * (N / (2 * tw)) * slices_waves64 >= 8192 * 64) tw *= 2;
+    int tw = 8;
+    while (tw < 256 && B * (N / (2 * tw)) * slices_waves64 >= 4096 * 64) tw *= 2;
     return tw;
 }
 
@@ -245,28 +300,44 @@ LookupGradPlan plan_lookup_grad(int64_t B, int64_t N, int64_t d, int64_t V, DTyp
 
 template <typename TI, typename TO>
 static hipError_t grad_launch(const TI* g, int64_t B, int64_t N, int64_t d, const int32_t* keys, const int32_t* order,
-                              int64_t V, const LookupGradPlan& p, float scale, TO* out, float* slot, hipStream_t s) {
+                              int64_t V, const LookupGradPlan& p, float scale, TO* out, float* slot, bool cleared,
+                              hipStream_t s) {
     const int C = row_chunks(d, sizeof(TI)), GL = group_lanes(C);
     const int slices = (C + GL - 1) / GL;
     const int64_t red = (p.npieces * slices * GL + kGradThreads - 1) / kGradThreads;
     // a clearing wave takes up to 64 KB of rows
     int64_t rz = 65536 / (d * (int64_t)sizeof(TO));
     rz = rz < 1 ? 1 : rz > 64 ? 64 : rz;
-    const int64_t clr = ((V + rz - 1) / rz + kGradThreads / 64 - 1) / (kGradThreads / 64);
+    const int64_t clr = cleared ? 0 : ((V + rz - 1) / rz + kGradThreads / 64 - 1) / (kGradThreads / 64);
     const dim3 grid((unsigned)(red + clr), (unsigned)B);
-#define KM_GO(G)                                                                                                  \
-    hipLaunchKernelGGL((k_lookup_grad<TI, TO, G>), grid, dim3(kGradThreads), 0, s, g, N, (int)d, C, keys, order, V, \
+    const bool stream = stream_out(B * V * d * (int64_t)sizeof(TO));
+#define KM_GO2(G, ST)                                                                                                 \
+    hipLaunchKernelGGL((k_lookup_grad<TI, TO, G, ST>), grid, dim3(kGradThreads), 0, s, g, N, (int)d, C, keys, order, V, \
                        p.tw, p.npieces, slices, red, (int)rz, scale, out, slot)
+#define KM_GO(G)                     \
+    do {                             \
+        if (stream) KM_GO2(G, true); \
+        else KM_GO2(G, false);       \
+    } while (0)
     if (GL == 8) KM_GO(8);
     else if (GL == 16) KM_GO(16);
     else if (GL == 32) KM_GO(32);
     else KM_GO(64);
 #undef KM_GO
+#undef KM_GO2
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || p.npieces < 2) return e;
-    const int fs = (C + 63) / 64;
-    hipLaunchKernelGGL((k_lookup_grad_fold<TI, TO>), dim3((unsigned)((p.npieces - 1) * fs), (unsigned)B),
-                       dim3(kGradThreads), 0, s, keys, N, (int)d, C, V, p.tw, p.npieces, fs, scale, out, slot);
+    const int ls = (C + 63) / 64;
+    const int64_t ft = fold_threads(GL), sb = ((p.npieces - 1) * slices * GL + ft - 1) / ft;
+    const int64_t lb = (p.npieces - 1) / kFoldShort * ls;
+#define KM_GO(G)                                                                                                     \
+    hipLaunchKernelGGL((k_lookup_grad_fold<TI, TO, G>), dim3((unsigned)(sb + lb), (unsigned)B), dim3((unsigned)ft),  \
+                       0, s, keys, N, (int)d, C, V, p.tw, p.npieces, slices, sb, ls, scale, out, slot)
+    if (GL == 8) KM_GO(8);
+    else if (GL == 16) KM_GO(16);
+    else if (GL == 32) KM_GO(32);
+    else KM_GO(64);
+#undef KM_GO
     return hipGetLastError();
 }
 
@@ -274,12 +345,17 @@ hipError_t launch_lookup_grad(DType xt, const void* g, int64_t B, int64_t N, int
                               int64_t V, float scale, DType gt, void* out, const LookupGradPlan& p, char* ws,
                               hipStream_t s) {
     if (B == 0) return hipSuccess;
-    const hipError_t e = launch_key_sort(labels, B, N, V, p.sort, ws, s);
+    // Few rows for the table's height: the whole gradient is cleared beside the
+    // one launch that ranks the labels (up to a quarter of the table written
+    // twice costs less than the search for the rows to clear).
+    const bool cleared = N > 0 && count_rank_fits(B, N) && 4 * N <= V;
+    const int64_t bytes = V * d * dtype_bytes(gt);
+    const hipError_t e = launch_key_sort(labels, B, N, V, p.sort, ws, s, cleared ? out : nullptr, bytes);
     if (e != hipSuccess) return e;
     const int32_t *keys = (int32_t*)(ws + p.sort.keys), *order = (int32_t*)(ws + p.sort.order);
     float* slot = (float*)(ws + p.slot);
 #define KM_GO(TI, TO) \
-    return grad_launch<TI, TO>((const TI*)g, B, N, d, keys, order, V, p, scale, (TO*)out, slot, s)
+    return grad_launch<TI, TO>((const TI*)g, B, N, d, keys, order, V, p, scale, (TO*)out, slot, cleared, s)
     if (xt == DType::F32) KM_GO(float, float);
     if (xt == DType::F16) {
         if (gt == DType::F32) KM_GO(_Float16, float);

@@ -14,7 +14,7 @@ constexpr int kRowThreads = 256;
 // out[i] = scale * table[labels[i]] (a label outside [0, V): zeros).  The
 // product is formed in float32 and rounded once.  U chunks per thread: the
 // label and then the row are two dependent loads, U of each are in flight.
-template <typename T, int U>
+template <typename T, int U, bool STREAM>
 __global__ __launch_bounds__(kRowThreads) void k_lookup(const T* __restrict__ table, int64_t V, int d, uint32_t C,
                                                         const int32_t* __restrict__ labels, int64_t N, int64_t BN,
                                                         float scale, T* __restrict__ out) {
@@ -43,9 +43,10 @@ __global__ __launch_bounds__(kRowThreads) void k_lookup(const T* __restrict__ ta
     for (int u = 0; u < U; ++u) {
         if (row[u] >= BN) continue;
         float a[VN];
+        const float f = lab[u] >= 0 && lab[u] < V ? scale : 0.f;  // (times zeros, where there is no label)
 #pragma unroll
-        for (int i = 0; i < VN; ++i) a[i] = (lab[u] >= 0 && lab[u] < V) ? scale * elem_f32(v[u][i]) : 0.f;
-        store_f32<T, VN>(out + row[u] * d + e0[u], d, a);
+        for (int i = 0; i < VN; ++i) a[i] = f * elem_f32(v[u][i]);
+        store_f32<T, VN, STREAM>(out + row[u] * d + e0[u], d, a);
     }
 }
 
@@ -56,20 +57,27 @@ hipError_t launch_lookup(DType xt, const void* table, int64_t B, int64_t V, int6
     const uint32_t C = row_chunks(d, dtype_bytes(xt));
     constexpr int U = 4;
     const int64_t blocks = (BN * C + kRowThreads * U - 1) / (kRowThreads * U);
-#define KM_GO(T)                                                                                              \
-    hipLaunchKernelGGL((k_lookup<T, U>), dim3((unsigned)blocks), dim3(kRowThreads), 0, s, (const T*)table, V, \
+    const bool stream = stream_out(BN * d * dtype_bytes(xt));
+#define KM_GO2(T, ST)                                                                                             \
+    hipLaunchKernelGGL((k_lookup<T, U, ST>), dim3((unsigned)blocks), dim3(kRowThreads), 0, s, (const T*)table, V, \
                        (int)d, C, labels, N, BN, scale, (T*)out)
+#define KM_GO(T)                    \
+    do {                            \
+        if (stream) KM_GO2(T, true); \
+        else KM_GO2(T, false);      \
+    } while (0)
     if (xt == DType::F32) KM_GO(float);
     else if (xt == DType::F16) KM_GO(_Float16);
     else KM_GO(uint16_t);
 #undef KM_GO
+#undef KM_GO2
     return hipGetLastError();
 }
 
 // rows[slots[t][k]] = x[t]: each token's chunk is read once and stored to its
 // `top` places.  The rows past the last slot (p >= *n_rows) become zero and
 // their order -1; they are handled by the thread whose token owns index p.
-template <typename T>
+template <typename T, bool STREAM>
 __global__ __launch_bounds__(kRowThreads) void k_dispatch(const T* __restrict__ x, int64_t Tn, int d, uint32_t C,
                                                           int top, const int32_t* __restrict__ slots,
                                                           const int32_t* __restrict__ n_rows, T* __restrict__ rows,
@@ -85,7 +93,7 @@ __global__ __launch_bounds__(kRowThreads) void k_dispatch(const T* __restrict__ 
     for (int k = 0; k < top; ++k) {
         const int64_t p = t * top + k;
         const int32_t sl = slots[p];
-        if (sl >= 0) store_raw<T>(rows + (int64_t)sl * d + e0, d, v);
+        if (sl >= 0) store_raw<T, STREAM>(rows + (int64_t)sl * d + e0, d, v);
         if (p >= n) {
             store_raw<T>(rows + p * d + e0, d, typename RowVec<T>::V{});
             if (c == 0) order[p] = -1;
@@ -98,13 +106,20 @@ hipError_t launch_dispatch_rows(DType xt, const void* x, int64_t T, int64_t d, i
     const uint32_t C = row_chunks(d, dtype_bytes(xt));
     const int64_t blocks = (T * C + kRowThreads - 1) / kRowThreads;
     if (blocks == 0) return hipSuccess;
+    const bool stream = stream_out(T * top * d * dtype_bytes(xt));
+#define KM_GO2(TT, ST)                                                                                             \
+    hipLaunchKernelGGL((k_dispatch<TT, ST>), dim3((unsigned)blocks), dim3(kRowThreads), 0, s, (const TT*)x, T, (int)d, \
+                       C, (int)top, slots, n_rows, (TT*)rows, order)
+#define KM_GO(TT)                     \
+    do {                              \
+        if (stream) KM_GO2(TT, true); \
+        else KM_GO2(TT, false);       \
+    } while (0)
     // a copy: 16-bit types share the instance
-    if (xt == DType::F32)
-        hipLaunchKernelGGL((k_dispatch<uint32_t>), dim3((unsigned)blocks), dim3(kRowThreads), 0, s, (const uint32_t*)x,
-                           T, (int)d, C, (int)top, slots, n_rows, (uint32_t*)rows, order);
-    else
-        hipLaunchKernelGGL((k_dispatch<uint16_t>), dim3((unsigned)blocks), dim3(kRowThreads), 0, s, (const uint16_t*)x,
-                           T, (int)d, C, (int)top, slots, n_rows, (uint16_t*)rows, order);
+    if (xt == DType::F32) KM_GO(uint32_t);
+    else KM_GO(uint16_t);
+#undef KM_GO
+#undef KM_GO2
     return hipGetLastError();
 }
 
@@ -234,12 +249,12 @@ hipError_t launch_dispatch_small(DType xt, const void* x, int64_t T, int64_t d, 
 
 // out[t] = sum_k w[t][k] rows[slots[t][k]] (w NULL: all 1), summed in float32
 // in the order of k and rounded once; a choice without a slot adds nothing.
-// Four rows are in flight per thread.
-template <typename T, bool WEIGHTED>
+// U rows are in flight per thread.
+template <typename T, bool WEIGHTED, int U, bool STREAM>
 __global__ __launch_bounds__(kRowThreads) void k_combine(const T* __restrict__ rows, int64_t Tn, int d, uint32_t C,
                                                          int top, const int32_t* __restrict__ slots,
                                                          const float* __restrict__ w, T* __restrict__ out) {
-    constexpr int VN = RowVec<T>::N, U = 4;
+    constexpr int VN = RowVec<T>::N;
     const ItemBase base = item_base(kRowThreads, C);
     int64_t t;
     int c;
@@ -272,7 +287,7 @@ __global__ __launch_bounds__(kRowThreads) void k_combine(const T* __restrict__ r
             for (int i = 0; i < VN; ++i) acc[i] = WEIGHTED ? fmaf(wk[u], elem_f32(v[u][i]), acc[i]) : acc[i] + elem_f32(v[u][i]);
         }
     }
-    store_f32<T, VN>(out + t * d + e0, d, acc);
+    store_f32<T, VN, STREAM>(out + t * d + e0, d, acc);
 }
 
 hipError_t launch_combine(DType xt, const void* rows, int64_t T, int64_t d, int64_t top, const int32_t* slots,
@@ -280,9 +295,21 @@ hipError_t launch_combine(DType xt, const void* rows, int64_t T, int64_t d, int6
     const uint32_t C = row_chunks(d, dtype_bytes(xt));
     const int64_t blocks = (T * C + kRowThreads - 1) / kRowThreads;
     if (blocks == 0) return hipSuccess;
-#define KM_GO2(TT, WT)                                                                                              \
-    hipLaunchKernelGGL((k_combine<TT, WT>), dim3((unsigned)blocks), dim3(kRowThreads), 0, s, (const TT*)rows, T, \
-                       (int)d, C, (int)top, slots, w, (TT*)out)
+    const bool stream = stream_out(T * d * dtype_bytes(xt));
+#define KM_GO4(TT, WT, U, ST)                                                                                        \
+    hipLaunchKernelGGL((k_combine<TT, WT, U, ST>), dim3((unsigned)blocks), dim3(kRowThreads), 0, s, (const TT*)rows, \
+                       T, (int)d, C, (int)top, slots, w, (TT*)out)
+#define KM_GO3(TT, WT, U)                     \
+    do {                                      \
+        if (stream) KM_GO4(TT, WT, U, true);  \
+        else KM_GO4(TT, WT, U, false);        \
+    } while (0)
+#define KM_GO2(TT, WT)                    \
+    do {                                  \
+        if (top <= 2) KM_GO3(TT, WT, 2);  \
+        else if (top <= 4) KM_GO3(TT, WT, 4); \
+        else KM_GO3(TT, WT, 8);           \
+    } while (0)
 #define KM_GO(TT)                \
     do {                         \
         if (w) KM_GO2(TT, true); \
@@ -293,6 +320,8 @@ hipError_t launch_combine(DType xt, const void* rows, int64_t T, int64_t d, int6
     else KM_GO(uint16_t);
 #undef KM_GO
 #undef KM_GO2
+#undef KM_GO3
+#undef KM_GO4
     return hipGetLastError();
 }
 
@@ -301,7 +330,7 @@ hipError_t launch_combine(DType xt, const void* rows, int64_t T, int64_t d, int6
 // float32: each lane sums its chunks in order, then a fixed tree over the
 // lanes and waves.  WPT waves per token; gy's chunk is read once for KB
 // choices.  Rows past the last slot (order < 0) become zero.
-template <typename T, int WPT>
+template <typename T, int WPT, bool STREAM>
 __global__ __launch_bounds__(kRowThreads) void k_combine_grad(const T* __restrict__ gy, const T* __restrict__ rows,
                                                               int64_t Tn, int d, int C, int top,
                                                               const int32_t* __restrict__ slots,
@@ -349,7 +378,7 @@ __global__ __launch_bounds__(kRowThreads) void k_combine_grad(const T* __restric
                         a[i] = wk[u] * gi;
                         if (i >= skip) dot[u] = fmaf(gi, elem_f32(r[u][i]), dot[u]);
                     }
-                    store_f32<T, VN>(grows + sl[u] * d + e0, d, a);
+                    store_f32<T, VN, STREAM>(grows + sl[u] * d + e0, d, a);
                 }
                 if (empty[u]) store_raw<T>(grows + (tt * top + k0 + u) * d + e0, d, typename RowVec<T>::V{});
             }
@@ -386,9 +415,15 @@ hipError_t launch_combine_grad(DType xt, const void* gy, const void* rows, int64
     if (T == 0) return hipSuccess;
     const int C = row_chunks(d, dtype_bytes(xt));
     const bool wide = C > 128;  // two chunks or more a lane: four waves share a token
-#define KM_GO2(TT, WPT)                                                                                              \
-    hipLaunchKernelGGL((k_combine_grad<TT, WPT>), dim3((unsigned)((T * (WPT) + 3) / 4)), dim3(kRowThreads), 0, s, \
-                       (const TT*)gy, (const TT*)rows, T, (int)d, C, (int)top, slots, order, w, (TT*)grows, gw)
+    const bool stream = stream_out(T * top * d * dtype_bytes(xt));
+#define KM_GO3(TT, WPT, ST)                                                                                        \
+    hipLaunchKernelGGL((k_combine_grad<TT, WPT, ST>), dim3((unsigned)((T * (WPT) + 3) / 4)), dim3(kRowThreads), 0, \
+                       s, (const TT*)gy, (const TT*)rows, T, (int)d, C, (int)top, slots, order, w, (TT*)grows, gw)
+#define KM_GO2(TT, WPT)                     \
+    do {                                    \
+        if (stream) KM_GO3(TT, WPT, true);  \
+        else KM_GO3(TT, WPT, false);        \
+    } while (0)
 #define KM_GO(TT)               \
     do {                        \
         if (wide) KM_GO2(TT, 4); \
@@ -399,6 +434,7 @@ hipError_t launch_combine_grad(DType xt, const void* gy, const void* rows, int64
     else KM_GO(uint16_t);
 #undef KM_GO
 #undef KM_GO2
+#undef KM_GO3
     return hipGetLastError();
 }
 
