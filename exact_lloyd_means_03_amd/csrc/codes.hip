@@ -96,80 +96,101 @@ __device__ __forceinline__ void store4(uint16_t* __restrict__ to, int64_t n, f32
 }
 
 // ---------------------------------------------------------------------------
-// Few rows per expert: the codes are streamed once, straight to registers.
+// The product.
 //
 // out[p][m]: D = W x^T on 16x16x32 matrix instructions, the weights as the
 // A operand.  Lane (r, q) of a tile (r < 16 row, q < 4) holds 16 bytes of
 // codes, the four words of its row's 32-column steps j, whose eight columns
-// q * 8 .. are exactly the eight values it supplies to step j: no exchange
-// between lanes.  Scales multiply the float32 sum of their group (GS groups
-// in a tile), so weights are never rounded after the codebook.
+// q * 8 .. are exactly the eight values it supplies to step j: the codes go
+// from memory to operands in registers, without LDS or an exchange between
+// lanes.  Scales multiply the float32 sum of their group (GS groups in a
+// tile), so weights are never rounded after the codebook.
 //
-// A block takes WR row tiles and 16 NT tokens, a wave one row tile and one of
-// WK parts of the columns; the columns go by in chunks of WK * U tiles, of
-// which a wave has U, all requested a chunk ahead.  With a row tile for every
-// wave (WK = 1) the tokens are read once for WR tiles and no sums are
-// exchanged; WK > 1 makes more waves where there are few row tiles, and the
-// parts are added in LDS in their order.
+// A block takes 16 R WR rows of the matrix and 16 NT tokens, a wave R row
+// tiles and one of WK parts of the columns.  The columns go by in chunks of
+// WK * U tiles, of which a wave has U, all requested a chunk ahead.  A weight
+// is decoded (25 instructions for eight) for 16 NT tokens, a token is read
+// from LDS for 16 R rows: large blocks where there is enough work to fill the
+// device with them, small ones elsewhere (launch rule below).  WK = 1
+// exchanges no sums; WK > 1 makes more waves where there are few row tiles,
+// and the parts are added in LDS in their order.
 //
-// XLDS: a chunk's tokens come to LDS by direct loads of whole lines (their
-// operand layout, 16 bytes from each of 16 rows, would cost a cache look-up
-// per lane), 16-byte chunks XOR-swizzled by the token against bank conflicts.
-// Otherwise (one token, whose loads are broadcasts, or rows without 16-byte
-// alignment) operands are loaded as they are.
-template <int WR, int WK, int U, int NT, int GS, bool XLDS>
+// X: how tokens come to the operands.  kXDirect: a chunk's tokens go to LDS by
+// direct loads of whole lines (the operand layout, 16 bytes from each of 16
+// rows, would cost a cache look-up per lane), 16-byte chunks XOR-swizzled by
+// the token against bank conflicts.  kXCopy: the same through registers, for
+// rows that do not start at 16-byte boundaries.  kXNone: operands straight
+// from memory, for one token (broadcasts).
+enum { kXNone, kXDirect, kXCopy };
+
+template <int WR, int WK, int U, int R, int NT, int GS, int X>
 struct ProductLds {
     static constexpr int TILE = 16 * NT * kCodeCols * 2;            // x of one tile
-    static constexpr int X = XLDS ? 2 * WK * U * TILE : 0;          // two chunks
-    static constexpr int SCALE = GS * 4 * 16 * 4;                   // a wave's scales: [4][GS][16]
-    static constexpr int SUMS = WK > 1 ? WR * WK * NT * 64 * 16 : 0;
-    static constexpr int LOOP = X + WR * WK * SCALE;
+    static constexpr int XB = X != kXNone ? 2 * WK * U * TILE : 0;  // two chunks
+    static constexpr int SCALE = GS * 64 * 4;                       // a wave's scales: [4 / R tiles][GS][16 R]
+    static constexpr int SUMS = WK > 1 ? WR * WK * R * NT * 64 * 16 : 0;
+    static constexpr int LOOP = XB + WR * WK * SCALE;
     static constexpr int BYTES = LOOP > SUMS ? LOOP : SUMS;
 };
 
-template <typename T, int WR, int WK, int U, int NT, int GS, bool XLDS>
+template <typename T, int WR, int WK, int U, int R, int NT, int GS, int X>
 __global__ __launch_bounds__(64 * WR * WK) void k_codes_product(
     const uint16_t* __restrict__ x, int64_t S, const char* __restrict__ codes, const uint16_t* __restrict__ table,
     int64_t table_rows, const uint16_t* __restrict__ scales, int64_t group, int64_t groups, int E, int64_t M,
     int64_t K, int64_t MT, int64_t KT, const int32_t* __restrict__ offsets, uint16_t* __restrict__ out) {
     typedef Half<T> H;
-    typedef ProductLds<WR, WK, U, NT, GS, XLDS> L;
+    typedef ProductLds<WR, WK, U, R, NT, GS, X> L;
+    constexpr bool XLDS = X != kXNone;
     constexpr int TT = 16 * NT, ROW = kCodeCols * 2, NG = GS ? GS : 1, W = WR * WK, CH = WK * U;
-    static_assert(U <= 4, "a quarter of the lanes loads a tile's scales");
+    static_assert(U * R <= 4, "16 R lanes load a tile's scales");
     extern __shared__ __attribute__((aligned(16))) char s_mem[];  // x, scales; then the sums
     const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wr = w / WK, wk = w % WK, r = lane & 15, q = lane >> 4;
-    float* s_scale = (float*)(s_mem + L::X + w * L::SCALE);  // [4][NG][16]
+    float* s_scale = (float*)(s_mem + L::XB + w * L::SCALE);  // [4 / R][NG][16 R]
     const Segment g = find_segment(offsets, S, E, TT, blockIdx.y);
     if (g.e < 0) return;
-    const int64_t mt = (int64_t)blockIdx.x * WR + wr;
-    f32x4 acc[NT];
+    const int64_t mt = ((int64_t)blockIdx.x * WR + wr) * R;  // the wave's first row tile
+    f32x4 acc[R][NT];
 #pragma unroll
-    for (int n = 0; n < NT; ++n) acc[n] = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int a = 0; a < R; ++a)
+#pragma unroll
+        for (int n = 0; n < NT; ++n) acc[a][n] = f32x4{0.f, 0.f, 0.f, 0.f};
     if (g.e < E) {  // (expert E stands for the rows past the last expert's)
-        const int64_t whole = K / kCodeCols, mc = mt < MT ? mt : MT - 1, mrow = mc * 16 + r < M ? mc * 16 + r : M - 1;
+        const int64_t whole = K / kCodeCols;
         const char* xs = (const char*)(x + g.p0 * K);
-        const char* cm = codes + ((int64_t)g.e * MT + mc) * KT * kCodeTile + lane * 16;
+        const char* cm[R];
+        Book book[R];
+#pragma unroll
+        for (int a = 0; a < R; ++a) {
+            const int64_t mc = mt + a < MT ? mt + a : MT - 1, m = mc * 16 + r < M ? mc * 16 + r : M - 1;
+            cm[a] = codes + ((int64_t)g.e * MT + mc) * KT * kCodeTile + lane * 16;
+            book[a] = load_book(table + (int64_t)g.e * table_rows * 16, table_rows, m);
+        }
         const uint16_t* xr[NT];
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
             const int t = n * 16 + r < g.n ? n * 16 + r : g.n - 1;  // absent tokens read the last one
             xr[n] = (const uint16_t*)xs + (int64_t)t * K + q * 8;
         }
-        const uint16_t* srow = GS ? scales + ((int64_t)g.e * M + mrow) * groups : nullptr;
-        // a wave's part of a chunk: U tiles of codes; lane (r, q): the scales of row r, tile q
+        // a wave's part of a chunk: U tiles of codes a row tile; lane l: the scales of row
+        // l % (16 R), tile l / (16 R)
+        const int64_t ms = mt * 16 + lane % (16 * R) < M ? mt * 16 + lane % (16 * R) : M - 1;
+        const uint16_t* srow = GS ? scales + ((int64_t)g.e * M + ms) * groups : nullptr;
+        const int stile = lane / (16 * R) < U ? lane / (16 * R) : U - 1;
         struct Part {
-            u32x4 cw[U];
+            u32x4 cw[R][U];
             uint16_t sc[NG];
         };
         auto fetch = [&](int64_t c0, Part& p) {
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 const int64_t kt = c0 + u * WK + wk;
-                p.cw[u] = *(const u32x4*)(cm + (kt < KT ? kt : KT - 1) * kCodeTile);
+#pragma unroll
+                for (int a = 0; a < R; ++a)
+                    p.cw[a][u] = *(const u32x4*)(cm[a] + (kt < KT ? kt : KT - 1) * kCodeTile);
             }
             if (GS) {
-                const int64_t kt = c0 + (U < 4 ? q % U : q) * WK + wk;
+                const int64_t kt = c0 + stile * WK + wk;
 #pragma unroll
                 for (int h = 0; h < NG; ++h) {
                     int64_t gi = GS == 1 ? kt * kCodeCols / group : kt * GS + h;
@@ -187,43 +208,52 @@ __global__ __launch_bounds__(64 * WR * WK) void k_codes_product(
                 const int64_t kt = c0 + ti;
                 if (id < NI && kt < whole) {
                     const int64_t src = tk < g.n ? tk : g.n - 1;
-                    dma16(xs, (uint32_t)(src * K * 2 + kt * ROW + ((lane & 15) ^ (tk & 15)) * 16),
-                          s_mem + buf * CH * L::TILE + id * 1024);
+                    const uint32_t from = (uint32_t)(src * K * 2 + kt * ROW + ((lane & 15) ^ (tk & 15)) * 16);
+                    char* to = s_mem + buf * CH * L::TILE + id * 1024;
+                    if (X == kXDirect) dma16(xs, from, to);
+                    else *(u32x4*)(to + lane * 16) = load8((const uint16_t*)(xs + from));
                 }
             }
         };
-        const Book book = load_book(table + (int64_t)g.e * table_rows * 16, table_rows, mrow);
         // tile kt from its codes and x; `at` is its place among the wave's scales.
         // END: the last tile of a row that is no multiple of 128 columns.
-        auto multiply = [&](int64_t kt, u32x4 cw, int at, const char* xl, auto end_tag) {
+        auto multiply = [&](int64_t kt, const Part& p, int u, const char* xl, auto end_tag) {
             constexpr bool END = decltype(end_tag)::value;
             const int left = (int)(K - kt * kCodeCols);
-            f32x4 part[NT];
+            u32x4 av[R][4];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                u32x4 xv[NT];
+            for (int a = 0; a < R; ++a)
 #pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    const uint16_t* p = xr[n] + kt * kCodeCols + j * 32;
-                    if constexpr (END) xv[n] = load8_end(p, left - j * 32 - q * 8);
-                    else if constexpr (XLDS) xv[n] = *(const u32x4*)(xl + (n * 16 + r) * ROW + ((j * 4 + q) ^ r) * 16);
-                    else xv[n] = load8(p);
+                for (int j = 0; j < 4; ++j) {
+                    av[a][j] = decode8(book[a], p.cw[a][u][j]);
+                    // columns past the row's end: x is zero there, and so must the weight be (0 * inf is no zero)
+                    if (END) av[a][j] = keep8(av[a][j], left - j * 32 - q * 8);
                 }
-                const bool start = GS && j % (4 / NG) == 0, end = GS && (j + 1) % (4 / NG) == 0;
-                u32x4 av = decode8(book, cw[j]);
-                // columns past the row's end: x is zero there, and so must the weight be (0 * inf is no zero)
-                if (END) av = keep8(av, left - j * 32 - q * 8);
-                f32x4 sv;
-                if (end) sv = *(const f32x4*)&s_scale[(at * NG + j * NG / 4) * 16 + q * 4];
 #pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    if (!GS) {
-                        acc[n] = H::mfma(av, xv[n], acc[n]);
-                    } else {
-                        part[n] = H::mfma(av, xv[n], start ? f32x4{0.f, 0.f, 0.f, 0.f} : part[n]);
-                        if (end) {
+            for (int n = 0; n < NT; ++n) {
+                u32x4 xv[4];
 #pragma unroll
-                            for (int i = 0; i < 4; ++i) acc[n][i] = fmaf(sv[i], part[n][i], acc[n][i]);
+                for (int j = 0; j < 4; ++j) {
+                    const uint16_t* p = xr[n] + kt * kCodeCols + j * 32;
+                    if constexpr (END) xv[j] = load8_end(p, left - j * 32 - q * 8);
+                    else if constexpr (XLDS) xv[j] = *(const u32x4*)(xl + (n * 16 + r) * ROW + ((j * 4 + q) ^ r) * 16);
+                    else xv[j] = load8(p);
+                }
+                f32x4 part[R];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const bool start = GS && j % (4 / NG) == 0, end = GS && (j + 1) % (4 / NG) == 0;
+#pragma unroll
+                    for (int a = 0; a < R; ++a) {
+                        if (!GS) acc[a][n] = H::mfma(av[a][j], xv[j], acc[a][n]);
+                        else part[a] = H::mfma(av[a][j], xv[j], start ? f32x4{0.f, 0.f, 0.f, 0.f} : part[a]);
+                    }
+                    if (end) {
+#pragma unroll
+                        for (int a = 0; a < R; ++a) {
+                            const f32x4 sv = *(const f32x4*)&s_scale[(u * NG + j * NG / 4) * 16 * R + a * 16 + q * 4];
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) acc[a][n][i] = fmaf(sv[i], part[a][i], acc[a][n][i]);
                         }
                     }
                 }
@@ -232,7 +262,7 @@ __global__ __launch_bounds__(64 * WR * WK) void k_codes_product(
         auto keep_scales = [&](const Part& p) {
             if (GS) {
 #pragma unroll
-                for (int h = 0; h < NG; ++h) s_scale[(q * NG + h) * 16 + r] = H::f32(p.sc[h]);
+                for (int h = 0; h < NG; ++h) s_scale[(lane / (16 * R) * NG + h) * 16 * R + lane % (16 * R)] = H::f32(p.sc[h]);
             }
         };
         Part p[2];
@@ -256,14 +286,14 @@ __global__ __launch_bounds__(64 * WR * WK) void k_codes_product(
                 for (int u = 0; u < U; ++u) {
                     const int64_t kt = c + u * WK + wk;
                     if (kt < whole)
-                        multiply(kt, p[b].cw[u], u, s_mem + (b * CH + u * WK + wk) * L::TILE, Tag<false>{});
+                        multiply(kt, p[b], u, s_mem + (b * CH + u * WK + wk) * L::TILE, Tag<false>{});
                 }
             }
         }
         if (whole < KT && whole % WK == wk) {
             fetch(whole - wk, p[0]);
             keep_scales(p[0]);
-            multiply(whole, p[0].cw[0], 0, nullptr, Tag<true>{});
+            multiply(whole, p[0], 0, nullptr, Tag<true>{});
         }
     }
     auto store = [&](int n, int64_t tile, int l, f32x4 v) {
@@ -273,199 +303,24 @@ __global__ __launch_bounds__(64 * WR * WK) void k_codes_product(
     };
     if constexpr (WK == 1) {
 #pragma unroll
-        for (int n = 0; n < NT; ++n) store(n, mt, lane, acc[n]);
+        for (int a = 0; a < R; ++a)
+#pragma unroll
+            for (int n = 0; n < NT; ++n) store(n, mt + a, lane, acc[a][n]);
     } else {
         __syncthreads();  // x and scales become the waves' sums
-        f32x4* sums = (f32x4*)s_mem;  // [WR][WK][NT][64]
+        f32x4* sums = (f32x4*)s_mem;  // [WR][WK][R][NT][64]
+        constexpr int PER = R * NT * 64;
 #pragma unroll
-        for (int n = 0; n < NT; ++n) sums[(w * NT + n) * 64 + lane] = acc[n];
+        for (int a = 0; a < R; ++a)
+#pragma unroll
+            for (int n = 0; n < NT; ++n) sums[((w * R + a) * NT + n) * 64 + lane] = acc[a][n];
         __syncthreads();
-        for (int i = threadIdx.x; i < WR * NT * 64; i += 64 * W) {
-            const int a = i / (NT * 64), rest = i % (NT * 64);
-            f32x4 v = sums[a * WK * NT * 64 + rest];
+        for (int i = threadIdx.x; i < WR * PER; i += 64 * W) {
+            const int row = i / PER, rest = i % PER;
+            f32x4 v = sums[row * WK * PER + rest];
 #pragma unroll
-            for (int o = 1; o < WK; ++o) v += sums[(a * WK + o) * NT * 64 + rest];
-            store(rest >> 6, (int64_t)blockIdx.x * WR + a, rest & 63, v);
-        }
-    }
-}
-
-// ---------------------------------------------------------------------------
-// Many rows per expert: a block of four waves takes 256 rows of the matrix by
-// 16 NT tokens.  Each wave decodes its own 64 rows, straight from the codes to
-// A operands as above, and multiplies them with every token of the block; so
-// a weight is decoded once per block and never stored.  The tokens' tile (16
-// NT rows of 128 columns, two buffers) comes to LDS by direct loads, its
-// 16-byte chunks XOR-swizzled by the row so that the 16 rows a B operand
-// reads lie on distinct banks.
-#ifndef PW
-#define PW 1
-#define PR 8
-#define PU 4
-#endif
-#ifndef GOCC
-#define GOCC 2
-#define GNT 6
-#define GSB 1
-#endif
-constexpr int kGemmWaves = 4, kGemmR = 4, kGemmOcc = GOCC, kGemmNT = GNT;  // waves, row tiles per wave
-
-template <typename T, int NT, int GS>
-__global__ __launch_bounds__(64 * kGemmWaves, kGemmOcc) void k_codes_gemm(
-    const uint16_t* __restrict__ x, int64_t S, const char* __restrict__ codes, const uint16_t* __restrict__ table,
-    int64_t table_rows, const uint16_t* __restrict__ scales, int64_t group, int64_t groups, int E, int64_t M,
-    int64_t K, int64_t MT, int64_t KT, const int32_t* __restrict__ offsets, uint16_t* __restrict__ out) {
-    typedef Half<T> H;
-    constexpr int R = kGemmR, TT = 16 * NT, ROW = kCodeCols * 2;
-    __shared__ __attribute__((aligned(16))) char s_x[2][TT * ROW];
-    __shared__ __attribute__((aligned(16))) uint32_t s_book[kGemmWaves * R * 16][8];
-    __shared__ __attribute__((aligned(16))) float s_scale[kGemmWaves][GS ? GS : 1][64];
-    const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
-    const int r = lane & 15, q = lane >> 4;
-    const Segment g = find_segment(offsets, S, E, TT, blockIdx.y);
-    if (g.e < 0) return;
-    const int64_t mt0 = ((int64_t)blockIdx.x * kGemmWaves + w) * R;  // the wave's first row tile
-    f32x4 acc[R][NT];
-#pragma unroll
-    for (int a = 0; a < R; ++a)
-#pragma unroll
-        for (int n = 0; n < NT; ++n) acc[a][n] = f32x4{0.f, 0.f, 0.f, 0.f};
-    if (g.e < E) {  // (block-uniform; expert E stands for the rows past the last expert's)
-        const char* xs = (const char*)(x + g.p0 * K);
-        // instruction i of the wave copies 1 KB: 4 token rows of 16 chunks
-        auto dma = [&](int64_t kt, int buf) {
-#pragma unroll
-            for (int i = 0; i < TT / 4 / kGemmWaves; ++i) {
-                const int t0 = (i * kGemmWaves + w) * 4;
-                const int t = t0 + (lane >> 4);
-                const int src = t < g.n ? t : g.n - 1;
-                const uint32_t off = (uint32_t)(src * K * 2 + kt * ROW + (((lane & 15) ^ (t & 15)) * 16));
-                dma16(xs, off, s_x[buf] + t0 * ROW);
-            }
-        };
-        // the last tile of a row that is no multiple of 128 columns: zeros past the row
-        auto copy_end = [&](int64_t kt, int buf) {
-            for (int i = threadIdx.x; i < TT * 16; i += 64 * kGemmWaves) {
-                const int t = i >> 4, c = i & 15;
-                const int src = t < g.n ? t : g.n - 1;
-                const int64_t k = kt * kCodeCols + c * 8;
-                *(u32x4*)(s_x[buf] + t * ROW + ((c ^ (t & 15)) * 16)) =
-                    load8_end((const uint16_t*)xs + src * K + k, (int)(K - k));
-            }
-        };
-        const int64_t whole = K / kCodeCols;
-        if (whole > 0) dma(0, 0);
-        const char* cm[R];
-#pragma unroll
-        for (int a = 0; a < R; ++a) {
-            const int64_t mt = mt0 + a < MT ? mt0 + a : MT - 1;  // absent tiles repeat the last one
-            cm[a] = codes + ((int64_t)g.e * MT + mt) * KT * kCodeTile + lane * 16;
-            if (q == 0) {
-                const int64_t m = mt * 16 + r < M ? mt * 16 + r : M - 1;
-                const Book b = load_book(table + (int64_t)g.e * table_rows * 16, table_rows, m);
-                uint32_t* to = s_book[(w * R + a) * 16 + r];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    to[i] = b.low[i];
-                    to[4 + i] = b.high[i];
-                }
-            }
-        }
-        u32x4 cw[R];
-#pragma unroll
-        for (int a = 0; a < R; ++a) cw[a] = *(const u32x4*)cm[a];
-        uint16_t sraw[GS ? GS : 1];
-        const int64_t ms = mt0 * 16 + lane < M ? mt0 * 16 + lane : M - 1;
-        const uint16_t* srow = GS ? scales + ((int64_t)g.e * M + ms) * groups : nullptr;
-        auto get_scales = [&](int64_t kt) {
-#pragma unroll
-            for (int h = 0; h < GS; ++h) {
-                int64_t gi = GS == 4 ? kt * 4 + h : GS == 2 ? kt * 2 + h : kt * kCodeCols / group;
-                if (gi >= groups) gi = groups - 1;
-                sraw[h] = srow[gi];
-            }
-        };
-        if (GS) get_scales(0);
-        __builtin_amdgcn_s_waitcnt(vmcnt_imm(0));
-        __syncthreads();
-        auto tile = [&](int64_t kt, int64_t next, int buf, auto end_tag) {
-            constexpr bool END = decltype(end_tag)::value;
-            // lane l's row: this tile's scales to the wave's slab, the next tile's requested
-            if (GS) {
-#pragma unroll
-                for (int h = 0; h < GS; ++h) s_scale[w][h][lane] = H::f32(sraw[h]);
-                get_scales(next);
-            }
-            const int left = (int)(K - kt * kCodeCols);
-            u32x4 av[R][4];
-#pragma unroll
-            for (int a = 0; a < R; ++a) {
-                Book b;
-                const u32x4* bp = (const u32x4*)s_book[(w * R + a) * 16 + r];
-                *(u32x4*)b.low = bp[0];
-                *(u32x4*)b.high = bp[1];
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    av[a][j] = decode8(b, cw[a][j]);
-                    if (END) av[a][j] = keep8(av[a][j], left - j * 32 - q * 8);
-                }
-            }
-#pragma unroll
-            for (int a = 0; a < R; ++a) cw[a] = *(const u32x4*)(cm[a] + next * kCodeTile);
-#pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                if (GSB) __builtin_amdgcn_sched_barrier(0);
-                u32x4 xv[4];
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    xv[j] = *(const u32x4*)(s_x[buf] + (n * 16 + r) * ROW + (((j * 4 + q) ^ r) * 16));
-                f32x4 part[R];
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const bool start = GS && j % (4 / (GS ? GS : 1)) == 0;
-                    const bool end = GS && (j + 1) % (4 / (GS ? GS : 1)) == 0;
-#pragma unroll
-                    for (int a = 0; a < R; ++a) {
-                        if (!GS) {
-                            acc[a][n] = H::mfma(av[a][j], xv[j], acc[a][n]);
-                        } else {
-                            part[a] = H::mfma(av[a][j], xv[j], start ? f32x4{0.f, 0.f, 0.f, 0.f} : part[a]);
-                        }
-                    }
-                    if (end) {
-#pragma unroll
-                        for (int a = 0; a < R; ++a) {
-                            const f32x4 sv = *(const f32x4*)&s_scale[w][j * (GS ? GS : 1) / 4][a * 16 + q * 4];
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) acc[a][n][i] = fmaf(sv[i], part[a][i], acc[a][n][i]);
-                        }
-                    }
-                }
-            }
-        };
-        for (int64_t kt = 0; kt < whole; ++kt) {
-            const int buf = (int)(kt & 1);
-            if (kt + 1 < whole) dma(kt + 1, buf ^ 1);
-            tile(kt, kt + 1 < KT ? kt + 1 : kt, buf, Tag<false>{});
-            // the next tile has landed before the barrier that publishes it
-            __builtin_amdgcn_s_waitcnt(vmcnt_imm(0));
-            __syncthreads();
-        }
-        if (whole < KT) {
-            copy_end(whole, 0);
-            __syncthreads();
-            tile(whole, whole, 0, Tag<true>{});
-        }
-    }
-#pragma unroll
-    for (int a = 0; a < R; ++a) {
-        const int64_t m = (mt0 + a) * 16 + q * 4;
-        if (m >= M) continue;
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-            const int t = n * 16 + r;
-            if (t >= g.n) continue;
-            store4<T>(out + (g.p0 + t) * M + m, M - m, acc[a][n]);
+            for (int o = 1; o < WK; ++o) v += sums[(row * WK + o) * PER + rest];
+            store(rest / 64 % NT, ((int64_t)blockIdx.x * WR + row) * R + rest / (64 * NT), rest & 63, v);
         }
     }
 }
@@ -478,40 +333,59 @@ static int groups_per_tile(const CodesArgs& a) {
     return a.group == 32 ? 4 : a.group == 64 ? 2 : 1;
 }
 
+// The launch: the largest block that still makes about one block for every
+// compute unit, among those whose tokens' tile is at least half full on
+// average over the experts.  Measured (bf16, groups of 128, us a call):
+//   tokens, matrices   16 x 32  16 x 128  32 x 64  32 x 128  64 x 128  128 x 128
+//     64, 4096 x 4096     14.7      23.5     17.0      25.8      33.3       54.8
+//    256, 4096 x 4096     49.4      41.1     28.1      28.4      35.1       56.0
+//    512, 4096 x 4096     93.7      75.9     53.5      47.7      37.4       57.3
+//   1024, 4096 x 4096    176.1     139.2    102.3      93.5      67.0       61.6
+//   2048, 4096 x 4096    328.9     259.5    194.2     167.0     130.6       95.2
+//     64, 8 of those      29.1      27.9     29.7      31.6      38.3       63.0
+//    512, 8 of those      97.4      74.5     54.2      47.6      39.5       63.5
+//   2048, 8 of those     354.2     261.2    189.5     164.6     119.6       93.3
+// (tokens x rows of a block).
 template <typename T>
 static hipError_t product_launch(const CodesArgs& a, hipStream_t s) {
     const int64_t MT = code_tiles_m(a.M), KT = code_tiles_k(a.K);
     const int64_t groups = a.scales ? (a.K + a.group - 1) / a.group : 0;
     const bool aligned = a.K % 8 == 0 && (uintptr_t)a.x % 16 == 0;
-    const bool many = a.S >= 64 * a.E && aligned;
+    const int64_t live = a.S < a.E ? a.S : a.E;  // experts with tokens, at most
+    auto fits = [&](int64_t tokens, int64_t rows) {
+        const int64_t blocks = (MT * 16 + rows - 1) / rows * live * ((a.S + live * tokens - 1) / (live * tokens));
+        return (tokens == 16 || 2 * a.S > tokens * a.E) && blocks >= 192;
+    };
     hipError_t e = hipSuccess;
-#define KM_ARGS                                                                                                      \
-    s, (const uint16_t*)a.x, a.S, (const char*)a.codes, (const uint16_t*)a.table, a.table_rows,                      \
-        (const uint16_t*)a.scales, a.group, groups, (int)a.E, a.M, a.K, MT, KT, a.offsets, (uint16_t*)a.out
-#define KM_MANY(GS)                                                                                                  \
-    hipLaunchKernelGGL((k_codes_gemm<T, kGemmNT, GS>),                                                               \
-                       dim3((unsigned)((MT + kGemmWaves * kGemmR - 1) / (kGemmWaves * kGemmR)),                      \
-                            (unsigned)segment_tiles(a.S, a.E, a.offsets, 16 * kGemmNT)),                             \
-                       dim3(64 * kGemmWaves), 0, KM_ARGS)
-#define KM_FEW(WR, WK, U, NT, GS, XLDS)                                                                              \
-    do {                                                                                                             \
-        constexpr size_t lds = ProductLds<WR, WK, U, NT, GS, XLDS>::BYTES;                                           \
-        if (lds > 64 * 1024 &&                                                                                       \
-            (e = hipFuncSetAttribute((const void*)k_codes_product<T, WR, WK, U, NT, GS, XLDS>,                       \
-                                     hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds)) != hipSuccess)           \
-            return e;                                                                                                \
-        hipLaunchKernelGGL((k_codes_product<T, WR, WK, U, NT, GS, XLDS>),                                            \
-                           dim3((unsigned)((MT + WR - 1) / WR), (unsigned)segment_tiles(a.S, a.E, a.offsets, 16 * NT)), \
-                           dim3(64 * WR * WK), lds, KM_ARGS);                                                        \
+#define KM_GO(WR, WK, U, R, NT, GS, X)                                                                                 \
+    do {                                                                                                              \
+        constexpr size_t lds = ProductLds<WR, WK, U, R, NT, GS, X>::BYTES;                                            \
+        if (lds > 64 * 1024 &&                                                                                        \
+            (e = hipFuncSetAttribute((const void*)k_codes_product<T, WR, WK, U, R, NT, GS, X>,                        \
+                                     hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds)) != hipSuccess)            \
+            return e;                                                                                                 \
+        hipLaunchKernelGGL((k_codes_product<T, WR, WK, U, R, NT, GS, X>),                                             \
+                           dim3((unsigned)((MT + WR * R - 1) / (WR * R)),                                             \
+                                (unsigned)segment_tiles(a.S, a.E, a.offsets, 16 * NT)),                               \
+                           dim3(64 * WR * WK), lds, s, (const uint16_t*)a.x, a.S, (const char*)a.codes,               \
+                           (const uint16_t*)a.table, a.table_rows, (const uint16_t*)a.scales, a.group, groups,        \
+                           (int)a.E, a.M, a.K, MT, KT, a.offsets, (uint16_t*)a.out);                                  \
     } while (0)
-    const int64_t row_tiles = MT * (a.S < a.E ? a.S : a.E);  // at most, over the experts
-#define KM_PICK(GS)                                                     \
-    do {                                                                \
-        if (many) KM_MANY(GS);                                          \
-        else if (a.S == 1 || !aligned) KM_FEW(1, 8, 4, 1, GS, false);   \
-        else if (row_tiles < 2048) KM_FEW(1, 8, 1, 1, GS, true);        \
-        else if (a.S > 16 * a.E) KM_FEW(PR, PW, PU, 2, GS, true);       \
-        else KM_FEW(PR, PW, PU, 1, GS, true);                           \
+#define KM_PICK(GS)                                                        \
+    do {                                                                   \
+        if (a.S == 1) KM_GO(1, 8, 4, 1, 1, GS, kXNone);                    \
+        else if (!aligned) {                                               \
+            if (fits(128, 128)) KM_GO(4, 1, 1, 2, 8, GS, kXCopy);          \
+            else if (fits(32, 128)) KM_GO(8, 1, 4, 1, 2, GS, kXCopy);      \
+            else KM_GO(1, 8, 1, 1, 1, GS, kXCopy);                         \
+        }                                                                  \
+        else if (fits(128, 128)) KM_GO(4, 1, 1, 2, 8, GS, kXDirect);       \
+        else if (fits(64, 128)) KM_GO(8, 1, 2, 1, 4, GS, kXDirect);        \
+        else if (fits(32, 128)) KM_GO(8, 1, 4, 1, 2, GS, kXDirect);        \
+        else if (fits(32, 64)) KM_GO(4, 2, 2, 1, 2, GS, kXDirect);         \
+        else if (fits(16, 128)) KM_GO(8, 1, 4, 1, 1, GS, kXDirect);        \
+        else if (fits(16, 32)) KM_GO(2, 4, 2, 1, 1, GS, kXDirect);         \
+        else KM_GO(1, 8, 1, 1, 1, GS, kXDirect);                           \
     } while (0)
     switch (groups_per_tile(a)) {
         case 0: KM_PICK(0); break;
@@ -520,9 +394,7 @@ static hipError_t product_launch(const CodesArgs& a, hipStream_t s) {
         default: KM_PICK(4); break;
     }
 #undef KM_PICK
-#undef KM_FEW
-#undef KM_MANY
-#undef KM_ARGS
+#undef KM_GO
     return hipGetLastError();
 }
 
@@ -626,7 +498,7 @@ __global__ __launch_bounds__(64 * kGradWaves) void k_codes_grad(
             // slots 0-3: codes of a row tile; 4, 5: 32 codebooks; 6 + h: scales; the rest repeat slot 0
             auto codes_of = [&](int i) {
                 const int64_t mt = st * (kGradRows / 16) + i;
-                dma16(ct, (uint32_t)((mt < MT ? mt : MT - 1) * KT * kCodeTile + lane * 16), to.codes + i * kCodeTile);
+                dma16(ct + (mt < MT ? mt : MT - 1) * KT * kCodeTile, lane * 16, to.codes + i * kCodeTile);
             };
             if (w < 4) {
                 codes_of(w);
@@ -641,8 +513,8 @@ __global__ __launch_bounds__(64 * kGradWaves) void k_codes_grad(
             if (GS && (w >= 6 || (GS == 4 && (w == 2 || w == 3))) && h < GS) {
                 int64_t gi = GS == 1 ? kt * kCodeCols / group : kt * GS + h;
                 if (gi >= groups) gi = groups - 1;
-                const int64_t m = m0 + lane < M ? m0 + lane : M - 1;
-                dma2(sc, (uint32_t)((m * groups + gi) * 2), to.scale[h]);
+                const int64_t row = m0 + lane < M ? lane : M - 1 - m0;
+                dma2(sc + m0 * groups * 2, (uint32_t)((row * groups + gi) * 2), to.scale[h]);
             }
         };
         // the wave's half of a row tile of step st, decoded and scaled, to a slab
