@@ -4,9 +4,9 @@ against plain float64 products.
 Bounds: a sum of n products of 16-bit values in float32, the scales applied to
 float32 partial sums: |err| <= 2 (n + 16) u32 sum|x W| + u |ref| (the factor 2
 and 16 for the roundings inside the matrix instructions, the scales' products
-and the join of partial sums).  Where the scaled weight is rounded to the
-16-bit type before the product (the gradient, and the product at many rows),
-each weight is off by u relative: u sum|x W| more.
+and the join of partial sums).  The gradient rounds the scaled weight to the
+16-bit type before the product, so each weight is off by u relative there:
+u sum|x W| more.
 """
 import numpy as np
 import pytest
@@ -103,11 +103,39 @@ def test_products(km, dtype, S, E, M, K, group, rows, used):
     out = torch.full((S, M), 7.0, dtype=dtype, device="cuda")
     got = km.kmeans_codes_product(x.cuda(), *args, M, sc, group, off, out=out)
     ref, mag = _ref(x, W, offsets, False)
-    _close(got, ref, mag, K, dtype, S > 64 and group > 0, "product")
+    _close(got, ref, mag, K, dtype, False, "product")
     out = torch.full((S, K), 7.0, dtype=dtype, device="cuda")
     got = km.kmeans_codes_product_grad(gy.cuda(), *args, K, sc, group, off, out=out)
     ref, mag = _ref(gy, W, offsets, True)
     _close(got, ref, mag, M, dtype, group > 0, "gradient")
+
+
+# One shape for each block the launches choose from (rows x columns of the
+# matrix, experts), with ragged rows, columns and tokens.
+BLOCKS = [  # S, E, M, K
+    (700, 1, 4128, 264), (700, 1, 4100, 640), (300, 1, 5000, 264), (150, 1, 5000, 648), (150, 1, 2600, 264),
+    (12, 6, 4200, 264), (12, 1, 6200, 136), (700, 1, 4128, 263), (150, 1, 5000, 517), (9, 1, 300, 1033),
+    (500, 1, 200, 8200), (300, 1, 130, 8200), (40, 1, 2000, 300), (1, 1, 3000, 130), (600, 3, 1100, 520),
+]
+
+
+@pytest.mark.parametrize("group", [0, 32, 64, 128])
+@pytest.mark.parametrize("S,E,M,K", BLOCKS)
+def test_products_of_every_block(km, S, E, M, K, group):
+    dtype = torch.float16 if (M + group) % 64 else torch.bfloat16
+    lab, table, scales, offsets, W = _case(S, E, M, K, group, dtype, "each", 30, S - S // 9)
+    g = torch.Generator().manual_seed(31)
+    x, gy = torch.randn((S, K), generator=g).to(dtype), torch.randn((S, M), generator=g).to(dtype)
+    args = (_packed(km, lab), table.cuda())
+    sc, off = None if scales is None else scales.cuda(), offsets.cuda()
+    got = km.kmeans_codes_product(x.cuda(), *args, M, sc, group, off, out=torch.full((S, M), 7.0, dtype=dtype, device="cuda"))
+    ref, mag = _ref(x, W, offsets, False)
+    _close(got, ref, mag, K, dtype, False, "product")
+    got = km.kmeans_codes_product_grad(gy.cuda(), *args, K, sc, group, off, out=torch.full((S, K), 7.0, dtype=dtype, device="cuda"))
+    ref, mag = _ref(gy, W, offsets, True)
+    _close(got, ref, mag, M, dtype, group > 0, "gradient")
+    again = km.kmeans_codes_product_grad(gy.cuda(), *args, K, sc, group, off)
+    assert torch.equal(got, again)
 
 
 @pytest.mark.parametrize("S", [1, 48, 600])
@@ -234,3 +262,29 @@ def test_codes_refusals(km):
         km.kmeans_codes_product(x, torch.stack([codes, codes]), torch.stack([table, table]), 16)
     with pytest.raises(ValueError, match="contiguous"):
         km.kmeans_codes_product_grad(x.t(), codes, table, 128)
+
+
+def test_codes_of_more_than_4_gb(km):
+    # tiles, scales and codebooks whose byte offsets pass 32 bits
+    M, K, group, dtype = 1 << 20, 8320, 128, torch.bfloat16
+    g = torch.Generator(device="cuda").manual_seed(20)
+    codes = torch.randint(0, 256, (M // 16, K // 128, 1024), generator=g, device="cuda", dtype=torch.uint8)
+    assert codes.numel() > 1 << 32
+    table = torch.randn((M, 16), generator=g, device="cuda").to(dtype)
+    scales = (0.5 + torch.rand((M, K // group), generator=g, device="cuda")).to(dtype)
+    rows = torch.tensor([0, 5, M // 2 + 3, M - 17, M - 1])
+    k = torch.arange(K)
+    # the code of (m, k) by the documented layout
+    j, q, i = k % 128 // 32, k % 32 // 8, k % 8
+    label = torch.stack([(codes[m // 16, (k // 128).cuda(), (((16 * q + m % 16) * 4 + j) * 4 + i % 4).cuda()].cpu().long()
+                          >> (4 * (i // 4))) & 15 for m in rows.tolist()])
+    W = torch.gather(table[rows.cuda()].cpu().double(), 1, label) * scales[rows.cuda()].cpu().double().repeat_interleave(group, 1)
+    for S in (1, 2):
+        x = torch.randn((S, K), generator=torch.Generator().manual_seed(21)).to(dtype)
+        y = km.kmeans_codes_product(x.cuda(), codes, table, M, scales, group)
+        _close(y[:, rows.cuda()], x.double() @ W.t(), x.double().abs() @ W.abs().t(), K, dtype, False, "large product")
+        gy = torch.zeros((S, M), dtype=dtype)
+        gy[:, rows] = torch.randn((S, len(rows)), generator=torch.Generator().manual_seed(22)).to(dtype)
+        gx = km.kmeans_codes_product_grad(gy.cuda(), codes, table, K, scales, group)
+        v = gy[:, rows].double()
+        _close(gx, v @ W, v.abs() @ W.abs(), len(rows), dtype, True, "large gradient")
