@@ -647,7 +647,10 @@ static GradShape grad_shape(int64_t S, int64_t E, int64_t M, int64_t K) {
     double least = 1e30;
     const double step_us[3] = {1.07, 1.26, 1.47};
     for (int i = 0; i < 3; ++i) {
-        const int64_t tt = 64 << i, blocks = code_tiles_k(K) * live * ((S + live * tt - 1) / (live * tt));
+        // token tiles: an expert's last one is half full on average
+        const int64_t tt = 64 << i, half = S / tt + (live + 1) / 2;
+        const int64_t tiles = E == 1 ? (S + tt - 1) / tt : half > live ? half : live;
+        const int64_t blocks = code_tiles_k(K) * tiles;
         for (int64_t n = 1; n <= 64 && (n == 1 || steps / n >= 4); n *= 2) {
             const double rounds = (double)((blocks * n + 255) / 256), per = (double)((steps + n - 1) / n);
             double us = rounds * (per * step_us[i] + 5.0);

@@ -91,10 +91,9 @@ km_status check_codes(int64_t S, int64_t E, int64_t M, int64_t K, int xt) {
     return KM_OK;
 }
 
-km_status run_codes(bool grad, const void* x, km_dtype xt_, int64_t S, const void* codes, const void* table,
+km_status run_codes(bool grad, const void* x, int xt, int64_t S, const void* codes, const void* table,
                     int64_t table_rows, const void* scales, int64_t group, int64_t E, int64_t M, int64_t K,
                     const int32_t* offsets, void* out, void* workspace, size_t workspace_bytes, km_stream stream) {
-    const int xt = enum_code(xt_);
     KM_TRY(check_codes(S, E, M, K, xt));
     if (table_rows != 1 && table_rows != M)
         return fail(KM_EINVAL, "table_rows must be 1 or M (table_rows=%lld M=%lld)", (long long)table_rows, (long long)M);
@@ -243,7 +242,7 @@ km_status kmeans_codes_product(const void* x, km_dtype xt, int64_t S, const void
                                int64_t table_rows, const void* scales, int64_t group, int64_t E, int64_t M, int64_t K,
                                const int32_t* offsets, void* out, void* workspace, size_t workspace_bytes,
                                km_stream stream) {
-    return run_codes(false, x, xt, S, codes, table, table_rows, scales, group, E, M, K, offsets, out, workspace,
+    return run_codes(false, x, enum_code(xt), S, codes, table, table_rows, scales, group, E, M, K, offsets, out, workspace,
                      workspace_bytes, stream);
 }
 
@@ -251,7 +250,7 @@ km_status kmeans_codes_product_grad(const void* grad, km_dtype xt, int64_t S, co
                                     int64_t table_rows, const void* scales, int64_t group, int64_t E, int64_t M,
                                     int64_t K, const int32_t* offsets, void* out, void* workspace,
                                     size_t workspace_bytes, km_stream stream) {
-    return run_codes(true, grad, xt, S, codes, table, table_rows, scales, group, E, M, K, offsets, out, workspace,
+    return run_codes(true, grad, enum_code(xt), S, codes, table, table_rows, scales, group, E, M, K, offsets, out, workspace,
                      workspace_bytes, stream);
 }
 
