@@ -360,7 +360,7 @@ struct KeySortPlan {
     size_t keys = 0, order = 0, keys2 = 0, order2 = 0, hist = 0, prefix = 0, counts = 0, total = 0;
 };
 KeySortPlan plan_key_sort(int64_t B, int64_t N, int64_t V);
-bool count_rank_fits(int64_t B, int64_t N);  // one launch ranks the labels
+bool count_rank_fits(int64_t B, int64_t N, int64_t V);  // one launch ranks the labels
 // clear (only where count_rank_fits): B times clear_bytes bytes to set to zero
 // beside the ranking.
 hipError_t launch_key_sort(const int32_t* labels, int64_t B, int64_t N, int64_t V, const KeySortPlan& p, char* ws,
@@ -369,8 +369,11 @@ hipError_t launch_key_sort(const int32_t* labels, int64_t B, int64_t N, int64_t 
 // Rows by label (rows.hip).
 hipError_t launch_lookup(DType xt, const void* table, int64_t B, int64_t V, int64_t d, const int32_t* labels,
                          int64_t N, float scale, void* out, hipStream_t s);
-// Choices up to which one launch sorts and copies.
-constexpr int64_t kDispatchSmall = 4096;
+// Few enough choices (M = T * top) for one launch that sorts and copies: its T
+// blocks each read M labels.  Against the counting pass and the copy, us a
+// call: T x M of 2^20 (1024 x 1024) 8.9 and 15.4, 2^21 (1024 x 2048) 11.5 and
+// 15.6, (512 x 4096) 15.7 and 15.4, 2^22 (2048 x 2048) 18.5 and 15.9.
+inline bool dispatch_small(int64_t T, int64_t M) { return M <= 4096 && T * M <= (int64_t)1 << 21; }
 hipError_t launch_dispatch_small(DType xt, const void* x, int64_t T, int64_t d, int64_t top, const int32_t* experts,
                                  int64_t E, void* rows, int32_t* offsets, int32_t* slots, int32_t* order,
                                  hipStream_t s);

@@ -6,9 +6,11 @@
 // for.  Both are built here from one counting pass over a digit of at most
 // 4097 values (k_digit_hist, the column scan of sort.hip, k_digit_rank):
 //   - routing: one pass over the experts, handing out each choice's place;
-//   - vocabularies: least significant digit first, ceil(bits / 12) passes,
-//     each stable, so that the last one leaves labels in ascending order and
-//     the indices of a label in ascending order.
+//   - vocabularies: least significant digit first, in one pass up to 4096
+//     labels and else ceil(bits / 12) passes, each stable, so that the last one
+//     leaves labels in ascending order and the indices of a label in ascending
+//     order.  131072 labels of 17 bits: two passes of 15 us, latency of
+//     dependent launches.
 // Short label vectors skip the passes: k_count_rank counts, for every label,
 // the ones that sort before it.
 //
@@ -241,8 +243,7 @@ hipError_t launch_route(const int32_t* experts, int64_t M, int64_t E, int32_t* H
 // equal keys of lower index.  A block ranks 64 entries (a lane each); its 16
 // waves split the problem's keys, read as LDS broadcasts.  In whole groups of
 // 64 keys before or after the block's own the index order is known, so a
-// key costs one compare and one add.  N^2 compares: 4 us at N = 8192, where
-// three launches a pass and two passes take three times that.
+// key costs one compare and one add.
 //
 // The blocks after the ranking ones clear `clear_bytes` bytes a problem at
 // `clear`, 64 KB each: memory the next launch wants zero, cleared beside the
@@ -315,7 +316,13 @@ static KeyDigits key_digits(int64_t V) {
     return {passes, bits, 1 << bits};
 }
 
-bool count_rank_fits(int64_t B, int64_t N) { return N <= 8192 && B * N * N <= ((int64_t)1 << 27); }
+// N^2 compares in one launch against three launches a pass.  A gradient by
+// either, us a call: V = 1000 (one pass) N = 4096 18.2 and 20.1, N = 8192 23.7
+// and 20.7; V = 32768 (two passes) N = 8192 30.9 and 37.4, N = 16384 47.4 and
+// 41.6; V = 131072 N = 8192 29.9 and 50.2, N = 16384 54.6 and 52.2.
+bool count_rank_fits(int64_t B, int64_t N, int64_t V) {
+    return N <= (key_digits(V).passes > 1 ? 8192 : 4096) && B * N * N <= ((int64_t)1 << 27);
+}
 
 KeySortPlan plan_key_sort(int64_t B, int64_t N, int64_t V) {
     KeySortPlan p;
@@ -328,7 +335,7 @@ KeySortPlan plan_key_sort(int64_t B, int64_t N, int64_t V) {
     const size_t BN = (size_t)B * N * sizeof(int32_t);
     p.keys = take(BN);
     p.order = take(BN);
-    if (!count_rank_fits(B, N)) {
+    if (!count_rank_fits(B, N, V)) {
         const KeyDigits g = key_digits(V);
         const size_t rows = (size_t)B * rank_chunks(B, N) * g.bins * sizeof(int32_t);
         p.hist = take(rows);
@@ -347,7 +354,7 @@ hipError_t launch_key_sort(const int32_t* labels, int64_t B, int64_t N, int64_t 
                            hipStream_t s, void* clear, int64_t clear_bytes) {
     if (B == 0 || N == 0) return hipSuccess;
     int32_t *keys = (int32_t*)(ws + p.keys), *order = (int32_t*)(ws + p.order);
-    if (count_rank_fits(B, N)) {
+    if (count_rank_fits(B, N, V)) {
         const int n64 = (int)((N + 63) / 64);
         const int64_t blocks = n64 + (clear ? (clear_bytes + kClearBlock - 1) / kClearBlock : 0);
         hipLaunchKernelGGL(k_count_rank, dim3((unsigned)blocks, (unsigned)B), dim3(kCountThreads),

@@ -62,9 +62,10 @@ struct DispatchPlan {
     size_t hist = 0, prefix = 0, counts = 0, total = 0;
 };
 
-DispatchPlan plan_dispatch(int64_t M, int64_t E) {
+DispatchPlan plan_dispatch(int64_t T, int64_t top, int64_t E) {
     DispatchPlan p;
-    if (M <= kDispatchSmall) return p;
+    const int64_t M = T * top;
+    if (dispatch_small(T, M)) return p;
     const size_t rows = align_up((size_t)rank_chunks(1, M) * E * sizeof(int32_t));
     p.prefix = rows;
     p.counts = 2 * rows;
@@ -156,7 +157,7 @@ km_status kmeans_lookup_grad(const void* grad, km_dtype xt_, int64_t B, int64_t 
 
 size_t kmeans_dispatch_workspace_bytes(int64_t T, int64_t top, int64_t E) {
     if (check_route(T, top) != KM_OK || check_experts(E) != KM_OK) return 0;
-    return plan_dispatch(T * top, E).total;
+    return plan_dispatch(T, top, E).total;
 }
 
 km_status kmeans_dispatch(const void* x, km_dtype xt_, int64_t T, int64_t d, const int32_t* experts, int64_t top,
@@ -173,10 +174,10 @@ km_status kmeans_dispatch(const void* x, km_dtype xt_, int64_t T, int64_t d, con
     KM_TRY(need(slots, T, "slots"));
     KM_TRY(need(order, T, "order"));
     const int64_t M = T * top;
-    const DispatchPlan p = plan_dispatch(M, E);
+    const DispatchPlan p = plan_dispatch(T, top, E);
     KM_TRY(check_ws_bytes(p.total, workspace, workspace_bytes));
     hipStream_t s = (hipStream_t)stream;
-    if (M <= kDispatchSmall) {
+    if (dispatch_small(T, M)) {
         KM_HIP(launch_dispatch_small((DType)xt, x, T, d, top, experts, E, rows, offsets, slots, order, s), "dispatch");
         return KM_OK;
     }
