@@ -541,33 +541,37 @@ def codes_workspace(S: int, E: int, M: int, K: int, dtype: torch.dtype, device) 
 
 
 def _codes_call(name, x, codes, table, M, K, scales, group, offsets, out, n_out, ws):
-    dev, S = x.device, x.shape[0]
+    dev, dt, S = x.device, x.dtype, x.shape[0]
     _tensor(codes, "codes", dev, torch.uint8, None)
-    if codes.dim() == 3:
+    tiles = (-(-M // 16), -(-K // 128), 1024)
+    shape = tuple(codes.shape)
+    if len(shape) == 4:
+        E, shape = shape[0], shape[1:]
+    elif len(shape) == 3:
         E = 1
-    elif codes.dim() == 4:
-        E = codes.shape[0]
     else:
         raise ValueError("codes must be [E, ceil(M / 16), ceil(K / 128), 1024] (or without E)")
-    if codes.shape[-3:] != (-(-M // 16), -(-K // 128), 1024):
-        raise ValueError(f"codes must be tiles {(-(-M // 16), -(-K // 128), 1024)}, got {tuple(codes.shape[-3:])}")
-    _tensor(table, "table", dev, x.dtype, None)
-    if table.dim() < 2 or table.shape[-1] != 16 or table.shape[-2] not in (1, M) or table.numel() != E * table.shape[-2] * 16:
+    if shape != tiles:
+        raise ValueError(f"codes must be tiles {tiles}, got {shape}")
+    _tensor(table, "table", dev, dt, None)
+    shape = tuple(table.shape)
+    rows = shape[-2] if len(shape) > 1 else 0
+    if (rows != M and rows != 1) or shape[-1] != 16 or table.numel() != E * rows * 16:
         raise ValueError("table must be [E, M, 16] or [E, 1, 16]")
     if scales is not None:
         groups = -(-K // group) if group > 0 else 0
-        _tensor(scales, "scales", dev, x.dtype, None)
-        if scales.dim() < 2 or scales.shape[-1] != groups or scales.shape[-2] != M or scales.numel() != E * M * groups:
+        _tensor(scales, "scales", dev, dt, None)
+        if tuple(scales.shape[-2:]) != (M, groups) or scales.numel() != E * M * groups:
             raise ValueError("scales must be [E, M, ceil(K / group)]")
     if offsets is not None:
         _tensor(offsets, "offsets", dev, torch.int32, (E + 1,))
     elif E != 1:
         raise ValueError("offsets are needed for more than one expert")
-    out = _output(out, "out", dev, x.dtype, (S, n_out))
-    ws = codes_workspace(S, E, M, K, x.dtype, dev) if ws is None else _tensor(ws, "workspace", dev, torch.uint8, None)
-    st = getattr(_lib.load(), name)(x.data_ptr(), _DT[x.dtype], S, codes.data_ptr(), table.data_ptr(),
-                                    table.shape[-2], _ptr(scales), group, E, M, K, _ptr(offsets), out.data_ptr(),
-                                    ws.data_ptr(), ws.numel(), _stream(dev))
+    out = _output(out, "out", dev, dt, (S, n_out))
+    ws = codes_workspace(S, E, M, K, dt, dev) if ws is None else _tensor(ws, "workspace", dev, torch.uint8, None)
+    st = getattr(_lib.load(), name)(x.data_ptr(), _DT[dt], S, codes.data_ptr(), table.data_ptr(), rows, _ptr(scales),
+                                    group, E, M, K, _ptr(offsets), out.data_ptr(), ws.data_ptr(), ws.numel(),
+                                    _stream(dev))
     if st:
         _lib.check(st, name)
     return out
