@@ -66,7 +66,6 @@ template <typename T>
 struct Half;
 template <>
 struct Half<_Float16> {
-    typedef _Float16 V8 __attribute__((ext_vector_type(8)));
     static __device__ __forceinline__ f32x4 mfma(u32x4 a, u32x4 b, f32x4 c) {
         return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
     }

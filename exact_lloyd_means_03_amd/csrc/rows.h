@@ -94,7 +94,7 @@ __device__ __forceinline__ void store_f32(T* __restrict__ p, int d, const float 
 }
 
 // Items (row, chunk) of a launch are numbered row-major; block b of threads
-// starts at item b * per_block.  ItemAt splits the item `off` places after
+// starts at item b * per_block.  item_at splits the item `off` places after
 // the block's first one without a 64-bit division per thread.
 struct ItemBase {
     int64_t row;
