@@ -71,14 +71,19 @@ constexpr uint32_t vmcnt_imm(int n) {  // s_waitcnt with only vmcnt <= n
 
 // One global_load_lds_dwordx4: lane l copies 16 bytes from sbase + voff to
 // LDS byte lds + 16 l (sbase and lds are wave-uniform: an SGPR pair and M0).
-// Written as a one-instruction asm statement so the compiler does not treat
-// the in-flight LDS write as aliasing every later LDS read (it would wait for
-// the copy right after issuing it); the kernel waits on vmcnt explicitly
-// before the barrier that publishes a tile.  The instruction has no register
-// results.
+// Written as an asm statement so the compiler does not treat the in-flight LDS
+// write as aliasing every later LDS read (it would wait for the copy right
+// after issuing it); the kernel waits on vmcnt explicitly before the barrier
+// that publishes a tile.  The load has no register results.
+//
+// The compiler keeps no distance between the instructions that write the
+// operands and an asm statement that reads them.  gfx9 wants five wait states
+// from a vector instruction's write of an SGPR (v_readfirstlane, or v_readlane
+// where the base was spilled) to a vector memory instruction's reading of it,
+// and one from a write of M0 to a load to LDS: s_nop 4 gives both.
 __device__ __forceinline__ void dma16(const char* sbase, uint32_t voff, const void* lds) {
     const uint32_t l = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) void*)lds;
-    asm volatile("global_load_lds_dwordx4 %0, %1" ::"v"(voff), "s"(sbase),
+    asm volatile("s_nop 4\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(voff), "s"(sbase),
                  "{m0}"(__builtin_amdgcn_readfirstlane(l))
                  : "memory");
 }
@@ -87,7 +92,7 @@ __device__ __forceinline__ void dma16(const char* sbase, uint32_t voff, const vo
 // word lds + 4 l (the high half becomes zero).
 __device__ __forceinline__ void dma2(const char* sbase, uint32_t voff, const void* lds) {
     const uint32_t l = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) void*)lds;
-    asm volatile("global_load_lds_ushort %0, %1" ::"v"(voff), "s"(sbase),
+    asm volatile("s_nop 4\n\tglobal_load_lds_ushort %0, %1" ::"v"(voff), "s"(sbase),
                  "{m0}"(__builtin_amdgcn_readfirstlane(l))
                  : "memory");
 }
