@@ -71,10 +71,54 @@ struct Half<_Float16> {
     }
     static __device__ __forceinline__ float f32(uint16_t v) { return (float)__builtin_bit_cast(_Float16, v); }
     static __device__ __forceinline__ uint16_t from(float v) { return __builtin_bit_cast(uint16_t, (_Float16)v); }
-    // the eight values of a word times s, each product rounded once
-    static __device__ __forceinline__ u32x4 decode_scaled(const Book& k, uint32_t w, uint16_t s) {
+    // A scaled weight v = s * entry reaches from 2^-48 to 2^32, float16 from
+    // 2^-14 to 2^16.  Weights are kept as 2^13 v where 2^-27 <= |v| < 4 (zeros
+    // too), and the others, which a step of the gradient takes in passes of their
+    // own, as 2^-16 v where |v| >= 4 (or NaN) and as 2^34 v below: normal
+    // numbers, rounded once, in all three windows.
+    static constexpr bool kWindows = true;
+    typedef _Float16 Scale;  // 2^13 s (exact, or infinite from |s| = 8 on)
+    static __device__ __forceinline__ Scale scale(uint16_t s) {
+        return __builtin_bit_cast(_Float16, s) * (_Float16)0x1p13f;
+    }
+    // the eight values of a word times s, each product rounded once: right where
+    // none of the codebook's entries strays
+    static __device__ __forceinline__ u32x4 decode_scaled(const Book& k, uint32_t w, Scale s) {
         typedef _Float16 H8 __attribute__((ext_vector_type(8)));
-        return __builtin_bit_cast(u32x4, __builtin_bit_cast(H8, decode8(k, w)) * (H8)__builtin_bit_cast(_Float16, s));
+        return __builtin_bit_cast(u32x4, __builtin_bit_cast(H8, decode8(k, w)) * (H8)s);
+    }
+    // How far the products of two entries with s lie from the normal numbers, a
+    // half each: 0x7800 or more is outside them (a zero entry or s stays inside,
+    // 0 times an infinite s does not).
+    typedef uint16_t U2 __attribute__((ext_vector_type(2)));
+    static __device__ __forceinline__ U2 strays(uint32_t entries, Scale s) {
+        typedef _Float16 H2 __attribute__((ext_vector_type(2)));
+        const uint32_t e = entries & 0x7fff7fffu, f = (__builtin_bit_cast(uint16_t, s) & 0x7fffu) * 0x10001u;
+        const U2 p = __builtin_bit_cast(U2, __builtin_bit_cast(H2, e) * __builtin_bit_cast(H2, f));
+        // 0x0400 where neither factor is zero (a nonzero f is larger): normal numbers, from
+        // there to 0x7bff, move to 0 .. 0x77ff, subnormal ones wrap
+        const U2 nonzero = __builtin_bit_cast(U2, ((e + 0x7fff7fffu) & 0x80008000u) >> 5);
+        return p - __builtin_elementwise_min(nonzero, __builtin_bit_cast(U2, f));
+    }
+    static __device__ __forceinline__ bool stray(U2 a) {
+        return __builtin_bit_cast(uint32_t, __builtin_elementwise_add_sat(a, (U2)0x0800)) & 0x80008000u;
+    }
+    // eight entries times s: the weights of a window alone, the others as zeros
+    static __device__ __forceinline__ u32x4 one_window(u32x4 x, float s, int window) {
+        const float by = window == 0 ? 0x1p13f : window == 1 ? 0x1p-16f : 0x1p34f;
+        u32x4 r;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            uint32_t h[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const float v = s * f32((uint16_t)(x[i] >> (16 * e)));  // (exact: 22 bits)
+                const int in = !(fabsf(v) < 4.f) ? 1 : v == 0.f || fabsf(v) >= 0x1p-27f ? 0 : 2;
+                h[e] = in == window ? from(v * by) : 0;
+            }
+            r[i] = h[0] | h[1] << 16;
+        }
+        return r;
     }
 };
 template <>
@@ -84,12 +128,15 @@ struct Half<__bf16> {
     }
     static __device__ __forceinline__ float f32(uint16_t v) { return bf16_to_f32(v); }
     static __device__ __forceinline__ uint16_t from(float v) { return __builtin_bit_cast(uint16_t, (__bf16)v); }
-    static __device__ __forceinline__ u32x4 decode_scaled(const Book& k, uint32_t w, uint16_t s) {
+    static constexpr bool kWindows = false;  // float32's range
+    typedef float Scale;
+    static __device__ __forceinline__ Scale scale(uint16_t s) { return bf16_to_f32(s); }
+    // the eight values of a word times s, each product rounded once
+    static __device__ __forceinline__ u32x4 decode_scaled(const Book& k, uint32_t w, Scale f) {
         typedef float F2 __attribute__((ext_vector_type(2)));
         typedef __bf16 B2 __attribute__((ext_vector_type(2)));
         uint32_t lo[2], hi[2];
         decode_planes(k, w, lo, hi);
-        const float f = bf16_to_f32(s);
         u32x4 r;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {

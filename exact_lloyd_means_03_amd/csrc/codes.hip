@@ -422,8 +422,13 @@ hipError_t launch_codes_product(DType xt, const CodesArgs& a, void*, hipStream_t
 // and the tiles' codes, codebooks and scales, comes by direct loads to LDS
 // whose lanes take consecutive addresses, one step ahead of its decoding.
 //
-// Scaled weights are rounded to the 16-bit type before the product: the scale
-// varies along the reduction, so it cannot wait for the float32 sum.
+// Scaled weights are rounded to the 16-bit type's precision before the
+// product: the scale varies along the reduction, so it cannot wait for the
+// float32 sum.  float16 lacks the range of a product of two of its numbers, so
+// weights are held there times 2^13, and a step that has any outside 2^-27 .. 4
+// takes its weights in three passes, each with a power of two of its own
+// (Half<_Float16>, codes.h).  Looking for such weights costs float16 8% of the
+// kernel's time (2048 tokens over 8 experts of 4096 x 2048: 99 us, bfloat16 93).
 //
 // Few tokens: the rows are split over blockIdx.z and the float32 partial sums
 // added in order by k_codes_grad_join.
@@ -464,11 +469,15 @@ __global__ __launch_bounds__(64 * kGradWaves) void k_codes_grad(
     float* __restrict__ part) {
     typedef Half<T> H;
     typedef short s16x4 __attribute__((ext_vector_type(4)));
+    typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
     constexpr int TT = kGradWaves / 2 * 16 * NTW, ROW = kCodeCols * 2, C = kCodeCols / 32, GROW = kGradRows * 2;
     extern __shared__ __attribute__((aligned(16))) char s_mem[];
     typedef GradStage<TT> Stage;
     Stage* stage = (Stage*)s_mem;                       // [3]
     auto slab = [&](int b) { return s_mem + 3 * sizeof(Stage) + b * (kGradRows * ROW); };
+    // does the step of a slab have weights in other windows: a byte a wave
+    constexpr bool WIN = GS && H::kWindows;
+    auto others = [&](int b) { return (uint8_t*)s_mem + 3 * sizeof(Stage) + 2 * kGradRows * ROW + b * kGradWaves; };
     const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int r = lane & 15, q = lane >> 4;
     const Segment sg = find_segment(offsets, S, E, TT, blockIdx.y);
@@ -529,23 +538,49 @@ __global__ __launch_bounds__(64 * kGradWaves) void k_codes_grad(
                 dma2(sc + m0 * groups * 2, (uint32_t)((row * groups + gi) * 2), to.scale[h]);
             }
         };
-        // the wave's half of a row tile of step st, decoded and scaled, to a slab
-        auto decode = [&](int64_t st, const Stage& from, char* to) {
+        // the wave's half of a row tile of step st, decoded and scaled, to slab b.
+        // ONE: the weights of one window alone.  Otherwise all, as if they lay in the
+        // first one, and a byte says whether they do: the lanes of a row share its
+        // codebook's entries out.
+        auto decode = [&](int64_t st, const Stage& from, int b, int window, auto one_tag) {
+            constexpr bool ONE = decltype(one_tag)::value;
             const int row = (w >> 1) * 16 + r;
             const uint2 cw = *(const uint2*)(from.codes + (w >> 1) * kCodeTile + lane * 16 + (w & 1) * 8);
             const u32x4* bk = (const u32x4*)(from.book + row * 32);
             const Book book = make_book(bk[0], bk[1]);
-            const bool there = st * kGradRows + row < M;
+            char* to = slab(b) + row * ROW;
+            const bool there = row < (int)(M - st * kGradRows);
+            bool stray = false;
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
                 const int jj = (w & 1) * 2 + j;
                 const uint32_t c = j ? cw.y : cw.x;
-                u32x4 a = GS ? H::decode_scaled(book, c, (uint16_t)from.scale[jj * GS / 4][row]) : decode8(book, c);
+                const uint16_t s = GS ? (uint16_t)from.scale[jj * GS / 4][row] : 0;
+                u32x4 a = GS && !ONE ? H::decode_scaled(book, c, H::scale(s)) : decode8(book, c);
+                if constexpr (WIN) {
+                    if constexpr (ONE) {
+                        a = H::one_window(a, H::f32(s), window);
+                    } else if (j == 0 || GS == 4) {  // (else both halves have one scale)
+                        const char* e = from.book + row * 32 + q * 8;
+                        if (GS == 1) {  // (and the waves of a row too)
+                            stray = H::stray(H::strays(*(const uint32_t*)(e + (w & 1) * 4), H::scale(s)));
+                        } else {
+                            const uint2 e2 = *(const uint2*)e;
+                            stray |= H::stray(__builtin_elementwise_max(H::strays(e2.x, H::scale(s)),
+                                                                        H::strays(e2.y, H::scale(s))));
+                        }
+                    }
+                }
                 if (!there) a = u32x4{0, 0, 0, 0};
-                *(u32x4*)(to + row * ROW + slab_chunk(jj * 4 + q, r) * 16) = a;
+                *(u32x4*)(to + slab_chunk(jj * 4 + q, r) * 16) = a;
             }
+            // (all lanes store the same byte: no branch between decoding and the product)
+            if (WIN && !ONE) others(b)[w] = __ballot(stray) != 0;
         };
-        auto multiply = [&](const char* w16, const Stage& from) {
+        // The slab's weights times the tokens.  ADD: a window's sums, brought to
+        // the first one's power of two.
+        auto multiply = [&](const char* w16, const Stage& from, float by, auto add_tag) {
+            constexpr bool ADD = decltype(add_tag)::value;
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 u32x4 gv[NTW];
@@ -569,8 +604,11 @@ __global__ __launch_bounds__(64 * kGradWaves) void k_codes_grad(
                         a[2 * f + 1] = __builtin_bit_cast(uint2, t).y;
                     }
 #pragma unroll
-                    for (int n = 0; n < NTW; ++n)
-                        acc[c][n] = H::mfma(u32x4{a[0], a[1], a[2], a[3]}, gv[n], acc[c][n]);
+                    for (int n = 0; n < NTW; ++n) {
+                        const u32x4 av = {a[0], a[1], a[2], a[3]};
+                        if constexpr (ADD) acc[c][n] += by * H::mfma(av, gv[n], f32x4{0.f, 0.f, 0.f, 0.f});
+                        else acc[c][n] = H::mfma(av, gv[n], acc[c][n]);
+                    }
                 }
             }
         };
@@ -581,14 +619,28 @@ __global__ __launch_bounds__(64 * kGradWaves) void k_codes_grad(
         fill(st0, stage[0]);
         landed();
         if (st0 + 1 < st1) fill(st0 + 1, stage[1]);
-        decode(st0, stage[0], slab(0));
+        decode(st0, stage[0], 0, 0, Tag<false>{});
         landed();
         int cur = 0, nxt = 1, far = 2, buf = 0;
         for (int64_t st = st0; st < st1; ++st) {
             // here slab `buf` holds step st and stage `nxt` step st + 1
+            const uint2 seen = WIN ? *(const uint2*)others(buf) : uint2{0, 0};
             if (st + 2 < st1) fill(st + 2, stage[far]);
-            if (st + 1 < st1) decode(st + 1, stage[nxt], slab(buf ^ 1));
-            multiply(slab(buf), stage[cur]);
+            if constexpr (WIN) {
+                if (__builtin_amdgcn_readfirstlane(seen.x | seen.y)) {  // (block-uniform)
+                    // the other windows, then the first one's weights alone for the usual way
+                    for (int window = 2; window >= 0; --window) {
+                        decode(st, stage[cur], buf, window, Tag<true>{});
+                        __syncthreads();
+                        if (window) {
+                            multiply(slab(buf), stage[cur], window == 1 ? 0x1p29f : 0x1p-21f, Tag<true>{});
+                            __syncthreads();
+                        }
+                    }
+                }
+            }
+            if (st + 1 < st1) decode(st + 1, stage[nxt], buf ^ 1, 0, Tag<false>{});
+            multiply(slab(buf), stage[cur], 1.f, Tag<false>{});
             landed();
             const int t = cur;
             cur = nxt;
@@ -605,6 +657,7 @@ __global__ __launch_bounds__(64 * kGradWaves) void k_codes_grad(
         for (int n = 0; n < NTW; ++n) {
             const int t = (th * NTW + n) * 16 + r;
             if (t >= sg.n) continue;
+            if (WIN) acc[c][n] *= 0x1p-13f;  // (exact)
             const int64_t at = (sg.p0 + t) * K + k;
             if (part) {
                 float* to = part + blockIdx.z * S * K + at;
@@ -694,7 +747,7 @@ static hipError_t grad_launch(const CodesArgs& a, void* ws, hipStream_t s) {
 #define KM_GO2(NTW, GS, DIR)                                                                                         \
     do {                                                                                                             \
         constexpr int TT = kGradWaves / 2 * 16 * NTW;                                                                \
-        const size_t lds = 3 * sizeof(GradStage<TT>) + 2 * kGradRows * kCodeCols * 2;                                \
+        const size_t lds = 3 * sizeof(GradStage<TT>) + 2 * kGradRows * kCodeCols * 2 + 2 * kGradWaves;               \
         if ((e = hipFuncSetAttribute((const void*)k_codes_grad<T, NTW, GS, DIR>,                                     \
                                      hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds)) != hipSuccess)           \
             return e;                                                                                                \

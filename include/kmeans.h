@@ -389,7 +389,12 @@ KM_API km_status kmeans_pack_codes(const int32_t *labels, int64_t M, int64_t K, 
  *   kmeans_codes_product        out[p][m] = sum_k x[p][k] W[e][m][k]
  *   kmeans_codes_product_grad   out[p][k] = sum_m x[p][m] W[e][m][k]
  * (the second is the gradient of the first's x).  Rows past offsets[E] become
- * zeros.  Sums are float32, rounded once at the end.
+ * zeros.  Sums are float32, rounded once at the end.  The first multiplies
+ * float32 sums by the scales; the second, with scales, rounds every
+ * W[e][m][k] once to xt's precision before it multiplies, whatever its size
+ * (float16: also products of scale and entry that float16 cannot hold;
+ * bfloat16: within float32's range), so that each is off by 2^-11 (KM_F16) or
+ * 2^-8 (KM_BF16) of itself at most.
  *   x        [S,K] (grad: [S,M]) of dtype xt: KM_F16 or KM_BF16.
  *   codes    E matrices of kmeans_codes_bytes(M, K) bytes, 16-byte aligned.
  *   table    [E,table_rows,16] of dtype xt: a codebook per row (table_rows ==
