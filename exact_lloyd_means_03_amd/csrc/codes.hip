@@ -333,6 +333,9 @@ __global__ __launch_bounds__(64 * WR * WK) void k_codes_product(
 
 size_t codes_product_scratch(int64_t, int64_t, int64_t, int64_t) { return 0; }
 
+// Groups of scales in a row (a group may be of any length: no sum with it).
+static int64_t groups_per_row(const CodesArgs& a) { return a.scales ? (a.K - 1) / a.group + 1 : 0; }
+
 // Groups of scales in a tile of 128 columns (1: a group spans whole tiles).
 static int groups_per_tile(const CodesArgs& a) {
     if (!a.scales) return 0;
@@ -355,7 +358,7 @@ static int groups_per_tile(const CodesArgs& a) {
 template <typename T>
 static hipError_t product_launch(const CodesArgs& a, hipStream_t s) {
     const int64_t MT = code_tiles_m(a.M), KT = code_tiles_k(a.K);
-    const int64_t groups = a.scales ? (a.K + a.group - 1) / a.group : 0;
+    const int64_t groups = groups_per_row(a);
     const bool aligned = a.K % 8 == 0 && (uintptr_t)a.x % 16 == 0;
     const int64_t live = a.S < a.E ? a.S : a.E;  // experts with tokens, at most
     auto fits = [&](int64_t tokens, int64_t rows) {
@@ -737,7 +740,7 @@ size_t codes_product_grad_scratch(int64_t S, int64_t E, int64_t M, int64_t K) {
 template <typename T>
 static hipError_t grad_launch(const CodesArgs& a, void* ws, hipStream_t s) {
     const int64_t MT = code_tiles_m(a.M), KT = code_tiles_k(a.K);
-    const int64_t groups = a.scales ? (a.K + a.group - 1) / a.group : 0;
+    const int64_t groups = groups_per_row(a);
     const GradShape shape = grad_shape(a.S, a.E, a.M, a.K);
     const int64_t nsplit = shape.splits, steps = (a.M + kGradRows - 1) / kGradRows;
     const int64_t per = (steps + nsplit - 1) / nsplit;

@@ -288,3 +288,19 @@ def test_codes_of_more_than_4_gb(km):
         gx = km.kmeans_codes_product_grad(gy.cuda(), codes, table, K, scales, group)
         v = gy[:, rows].double()
         _close(gx, v @ W, v.abs() @ W.abs(), len(rows), dtype, True, "large gradient")
+
+
+def test_a_group_of_any_length(km):
+    # one group holds the row: the longest length that an int64 holds is as good as the row's own
+    S, E, M, K = 20, 2, 48, 300
+    lab, table, scales, offsets, W = _case(S, E, M, K, 384, torch.bfloat16, "each", 40)
+    g = torch.Generator().manual_seed(41)
+    x, gy = torch.randn((S, K), generator=g).to(torch.bfloat16), torch.randn((S, M), generator=g).to(torch.bfloat16)
+    args = (_packed(km, lab), table.cuda())
+    for group in (384, (1 << 63) - 128):
+        y = km.kmeans_codes_product(x.cuda(), *args, M, scales.cuda(), group, offsets.cuda())
+        ref, mag = _ref(x, W, offsets, False)
+        _close(y, ref, mag, K, torch.bfloat16, False, f"product, group {group}")
+        gx = km.kmeans_codes_product_grad(gy.cuda(), *args, K, scales.cuda(), group, offsets.cuda())
+        ref, mag = _ref(gy, W, offsets, True)
+        _close(gx, ref, mag, M, torch.bfloat16, True, f"gradient, group {group}")
