@@ -3,14 +3,16 @@
 // every row of weights clustered to 16 values; and of the wpnews.pro "Cache-
 // Aware Weight Clustering" post: products straight on codebook and indices).
 #include "codes.h"
+#include "rows.h"
 
 namespace km {
 
 // labels [M][K] -> tiles (layout in include/kmeans.h).  One thread per 32-bit
 // word: 16 bytes per lane and tile, consecutive lanes consecutive words.
 __global__ __launch_bounds__(256) void k_pack_codes(const int32_t* __restrict__ labels, int64_t M, int64_t K,
-                                                    int64_t KT, int64_t words, uint32_t* __restrict__ codes) {
-    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+                                                    int64_t KT, int64_t words, uint32_t* __restrict__ codes,
+                                                   int64_t block0) {
+    const int64_t i = (block0 + blockIdx.x) * 256 + threadIdx.x;
     if (i >= words) return;
     const int64_t tile = i >> 8;
     const int wd = (int)(i & 255), j = wd & 3, lane = wd >> 2;
@@ -27,8 +29,9 @@ __global__ __launch_bounds__(256) void k_pack_codes(const int32_t* __restrict__ 
 hipError_t launch_pack_codes(const int32_t* labels, int64_t M, int64_t K, void* codes, hipStream_t s) {
     const int64_t KT = code_tiles_k(K), words = code_tiles_m(M) * KT * (kCodeTile / 4);
     if (words == 0) return hipSuccess;
-    hipLaunchKernelGGL(k_pack_codes, dim3((unsigned)((words + 255) / 256)), dim3(256), 0, s, labels, M, K, KT, words,
-                       (uint32_t*)codes);
+    in_launches((words + 255) / 256, [&](int64_t b0, unsigned n) {
+        hipLaunchKernelGGL(k_pack_codes, dim3(n), dim3(256), 0, s, labels, M, K, KT, words, (uint32_t*)codes, b0);
+    });
     return hipGetLastError();
 }
 

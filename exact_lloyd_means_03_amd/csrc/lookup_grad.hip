@@ -350,9 +350,10 @@ hipError_t launch_lookup_grad(DType xt, const void* g, int64_t B, int64_t N, int
     if (B == 0) return hipSuccess;
     // Few rows for the table's height: the whole gradient is cleared beside the
     // one launch that ranks the labels (up to a quarter of the table written
-    // twice costs less than the search for the rows to clear).
-    const bool cleared = N > 0 && count_rank_fits(B, N, V) && 4 * N <= V;
+    // twice costs less than the search for the rows to clear), where one launch
+    // has the threads for it (1024 for 64 KB).
     const int64_t bytes = V * d * dtype_bytes(gt);
+    const bool cleared = N > 0 && count_rank_fits(B, N, V) && 4 * N <= V && bytes < (int64_t)1 << 37;
     const hipError_t e = launch_key_sort(labels, B, N, V, p.sort, ws, s, cleared ? out : nullptr, bytes);
     if (e != hipSuccess) return e;
     const int32_t *keys = (int32_t*)(ws + p.sort.keys), *order = (int32_t*)(ws + p.sort.order);

@@ -19,8 +19,8 @@ km_status check_dtype(int xt) {
     return KM_OK;
 }
 
-// n rows of d elements: non-negative, below 2^31 rows and with few enough
-// 16-byte chunks that one launch of 256-thread blocks covers them.
+// n rows of d elements: non-negative, below 2^31 rows, and of fewer 16-byte
+// chunks (8 TB) than the kernels' index arithmetic allows for.
 km_status check_rows(int64_t n, int64_t d, int xt, const char* what) {
     KM_TRY(check_dtype(xt));
     if (n < 0) return fail(KM_EINVAL, "negative number of %s: %lld", what, (long long)n);

@@ -93,6 +93,16 @@ __device__ __forceinline__ void store_f32(T* __restrict__ p, int d, const float 
     }
 }
 
+// A launch has fewer than 2^32 threads (hipLaunchKernel's limit in a dimension
+// of the grid): more blocks than kLaunchBlocks of 256 threads are launched in
+// parts, launch(first block, blocks).
+constexpr int64_t kLaunchBlocks = (int64_t)1 << 22;
+template <typename F>
+inline void in_launches(int64_t blocks, F launch) {
+    for (int64_t b0 = 0; b0 < blocks; b0 += kLaunchBlocks)
+        launch(b0, (unsigned)(blocks - b0 < kLaunchBlocks ? blocks - b0 : kLaunchBlocks));
+}
+
 // Items (row, chunk) of a launch are numbered row-major; block b of threads
 // starts at item b * per_block.  item_at splits the item `off` places after
 // the block's first one without a 64-bit division per thread.
@@ -100,8 +110,8 @@ struct ItemBase {
     int64_t row;
     uint32_t chunk;
 };
-__device__ __forceinline__ ItemBase item_base(int64_t per_block, uint32_t C) {
-    const uint64_t first = (uint64_t)blockIdx.x * (uint64_t)per_block;
+__device__ __forceinline__ ItemBase item_base(int64_t block0, int64_t per_block, uint32_t C) {
+    const uint64_t first = (uint64_t)(block0 + blockIdx.x) * (uint64_t)per_block;
     const uint64_t r = first / C;
     return {(int64_t)r, (uint32_t)(first - r * C)};
 }

@@ -19,9 +19,9 @@ constexpr int kRowThreads = 256;
 template <typename T, int U, bool STREAM>
 __global__ __launch_bounds__(kRowThreads) void k_lookup(const T* __restrict__ table, int64_t V, int d, uint32_t C,
                                                         const int32_t* __restrict__ labels, int64_t N, int64_t BN,
-                                                        float scale, T* __restrict__ out) {
+                                                        float scale, T* __restrict__ out, int64_t block0) {
     constexpr int VN = RowVec<T>::N;
-    const ItemBase base = item_base((int64_t)kRowThreads * U, C);
+    const ItemBase base = item_base(block0, (int64_t)kRowThreads * U, C);
     int64_t row[U];
     int e0[U];
     int32_t lab[U];
@@ -60,9 +60,11 @@ hipError_t launch_lookup(DType xt, const void* table, int64_t B, int64_t V, int6
     constexpr int U = 4;
     const int64_t blocks = (BN * C + kRowThreads * U - 1) / (kRowThreads * U);
     const bool stream = stream_out(BN * d * dtype_bytes(xt));
-#define KM_GO2(T, ST)                                                                                             \
-    hipLaunchKernelGGL((k_lookup<T, U, ST>), dim3((unsigned)blocks), dim3(kRowThreads), 0, s, (const T*)table, V, \
-                       (int)d, C, labels, N, BN, scale, (T*)out)
+#define KM_GO2(T, ST)                                                                                            \
+    in_launches(blocks, [&](int64_t b0, unsigned n) {                                                            \
+        hipLaunchKernelGGL((k_lookup<T, U, ST>), dim3(n), dim3(kRowThreads), 0, s, (const T*)table, V, (int)d, C, \
+                           labels, N, BN, scale, (T*)out, b0);                                                   \
+    })
 #define KM_GO(T)                    \
     do {                            \
         if (stream) KM_GO2(T, true); \
@@ -84,8 +86,8 @@ template <typename T, bool STREAM>
 __global__ __launch_bounds__(kRowThreads) void k_dispatch(const T* __restrict__ x, int64_t Tn, int d, uint32_t C,
                                                           int top, const int32_t* __restrict__ slots,
                                                           const int32_t* __restrict__ n_rows, T* __restrict__ rows,
-                                                          int32_t* __restrict__ order) {
-    const ItemBase base = item_base(kRowThreads, C);
+                                                          int32_t* __restrict__ order, int64_t block0) {
+    const ItemBase base = item_base(block0, kRowThreads, C);
     int64_t t;
     int c;
     item_at(base, threadIdx.x, C, &t, &c);
@@ -111,8 +113,10 @@ hipError_t launch_dispatch_rows(DType xt, const void* x, int64_t T, int64_t d, i
     if (blocks == 0) return hipSuccess;
     const bool stream = stream_out(T * top * d * dtype_bytes(xt));
 #define KM_GO2(TT, ST)                                                                                             \
-    hipLaunchKernelGGL((k_dispatch<TT, ST>), dim3((unsigned)blocks), dim3(kRowThreads), 0, s, (const TT*)x, T, (int)d, \
-                       C, (int)top, slots, n_rows, (TT*)rows, order)
+    in_launches(blocks, [&](int64_t b0, unsigned n) {                                                              \
+        hipLaunchKernelGGL((k_dispatch<TT, ST>), dim3(n), dim3(kRowThreads), 0, s, (const TT*)x, T, (int)d, C,     \
+                           (int)top, slots, n_rows, (TT*)rows, order, b0);                                         \
+    })
 #define KM_GO(TT)                     \
     do {                              \
         if (stream) KM_GO2(TT, true); \
@@ -258,9 +262,9 @@ hipError_t launch_dispatch_small(DType xt, const void* x, int64_t T, int64_t d, 
 template <typename T, bool WEIGHTED, int U, bool STREAM>
 __global__ __launch_bounds__(kRowThreads) void k_combine(const T* __restrict__ rows, int64_t Tn, int d, uint32_t C,
                                                          int top, const int32_t* __restrict__ slots,
-                                                         const float* __restrict__ w, T* __restrict__ out) {
+                                                         const float* __restrict__ w, T* __restrict__ out, int64_t block0) {
     constexpr int VN = RowVec<T>::N;
-    const ItemBase base = item_base(kRowThreads, C);
+    const ItemBase base = item_base(block0, kRowThreads, C);
     int64_t t;
     int c;
     item_at(base, threadIdx.x, C, &t, &c);
@@ -301,9 +305,11 @@ hipError_t launch_combine(DType xt, const void* rows, int64_t T, int64_t d, int6
     const int64_t blocks = (T * C + kRowThreads - 1) / kRowThreads;
     if (blocks == 0) return hipSuccess;
     const bool stream = stream_out(T * d * dtype_bytes(xt));
-#define KM_GO4(TT, WT, U, ST)                                                                                        \
-    hipLaunchKernelGGL((k_combine<TT, WT, U, ST>), dim3((unsigned)blocks), dim3(kRowThreads), 0, s, (const TT*)rows, \
-                       T, (int)d, C, (int)top, slots, w, (TT*)out)
+#define KM_GO4(TT, WT, U, ST)                                                                                       \
+    in_launches(blocks, [&](int64_t b0, unsigned n) {                                                               \
+        hipLaunchKernelGGL((k_combine<TT, WT, U, ST>), dim3(n), dim3(kRowThreads), 0, s, (const TT*)rows, T, (int)d, \
+                           C, (int)top, slots, w, (TT*)out, b0);                                                    \
+    })
 #define KM_GO3(TT, WT, U)                     \
     do {                                      \
         if (stream) KM_GO4(TT, WT, U, true);  \
@@ -342,11 +348,11 @@ __global__ __launch_bounds__(kRowThreads) void k_combine_grad(const T* __restric
                                                               const int32_t* __restrict__ slots,
                                                               const int32_t* __restrict__ order,
                                                               const float* __restrict__ w, T* __restrict__ grows,
-                                                              float* __restrict__ gw) {
+                                                              float* __restrict__ gw, int64_t block0) {
     constexpr int VN = RowVec<T>::N, KB = 4, NW = kRowThreads / 64;
     __shared__ float s_dot[NW][KB];
     const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
-    const int64_t t = (int64_t)blockIdx.x * (NW / WPT) + wv / WPT;
+    const int64_t t = (block0 + blockIdx.x) * (NW / WPT) + wv / WPT;
     if (WPT < NW && t >= Tn) return;  // (WPT == NW: every block has a token)
     const int64_t S = Tn * top;
     const int64_t tt = t;
@@ -422,9 +428,11 @@ hipError_t launch_combine_grad(DType xt, const void* gy, const void* rows, int64
     const int C = row_chunks(d, dtype_bytes(xt));
     const bool wide = C > 128;  // two chunks or more a lane: four waves share a token
     const bool stream = stream_out(T * top * d * dtype_bytes(xt));
-#define KM_GO3(TT, WPT, ST)                                                                                        \
-    hipLaunchKernelGGL((k_combine_grad<TT, WPT, ST>), dim3((unsigned)((T * (WPT) + 3) / 4)), dim3(kRowThreads), 0, \
-                       s, (const TT*)gy, (const TT*)rows, T, (int)d, C, (int)top, slots, order, w, (TT*)grows, gw)
+#define KM_GO3(TT, WPT, ST)                                                                                         \
+    in_launches((T * (WPT) + 3) / 4, [&](int64_t b0, unsigned n) {                                                  \
+        hipLaunchKernelGGL((k_combine_grad<TT, WPT, ST>), dim3(n), dim3(kRowThreads), 0, s, (const TT*)gy,          \
+                           (const TT*)rows, T, (int)d, C, (int)top, slots, order, w, (TT*)grows, gw, b0);           \
+    })
 #define KM_GO2(TT, WPT)                     \
     do {                                    \
         if (stream) KM_GO3(TT, WPT, true);  \
