@@ -13,6 +13,10 @@ constexpr int64_t kMaxB = 65535;
 constexpr int64_t kMaxInt = 0x7fffffff;
 constexpr int64_t kMaxV = (int64_t)1 << 30;
 constexpr int64_t kMaxSide = (int64_t)1 << 20;  // rows or columns of a 4-bit matrix
+// Rows of a 4-bit product: its token tiles go in the grid's second axis (65535
+// at most).  Tiles of 16 tokens are taken for 2^16 rows or less, whatever the
+// matrices, so there are never more than 2^20 / 32 + kRouteMaxE + 1 of them.
+constexpr int64_t kMaxTokens = (int64_t)1 << 20;
 
 km_status check_dtype(int xt) {
     if (xt != KM_F32 && xt != KM_F16 && xt != KM_BF16) return fail(KM_EUNSUPPORTED, "unknown dtype %d", xt);
@@ -86,9 +90,7 @@ km_status check_codes(int64_t S, int64_t E, int64_t M, int64_t K, int xt) {
     KM_TRY(check_matrix(M, K));
     KM_TRY(check_dtype(xt));
     if (xt == KM_F32) return fail(KM_EUNSUPPORTED, "products with 4-bit weights take 16-bit rows, not float32");
-    if (S > kMaxInt) return fail(KM_EUNSUPPORTED, "S=%lld >= 2^31 is not supported", (long long)S);
-    // token tiles of 16 rows or more go in the grid's second axis
-    if (S / 16 + E + 1 > 65535) return fail(KM_EUNSUPPORTED, "S=%lld rows are not supported in one call", (long long)S);
+    if (S > kMaxTokens) return fail(KM_EUNSUPPORTED, "S=%lld > 2^20 is not supported", (long long)S);
     return KM_OK;
 }
 

@@ -404,7 +404,7 @@ KM_API km_status kmeans_pack_codes(const int32_t *labels, int64_t M, int64_t K, 
  *   offsets  [E+1] int32, ascending from 0, offsets[E] <= S; NULL with E == 1
  *            means all S rows.
  *   out      [S,M] (grad: [S,K]) of dtype xt.
- * S < 2^31, E <= 4096, M, K <= 2^20.  The workspace must hold
+ * S, M, K <= 2^20, E <= 4096.  The workspace must hold
  * kmeans_codes_workspace_bytes(S, E, M, K, xt) bytes, 256-byte aligned (0
  * from the query: none is needed, or the shapes are invalid). */
 KM_API size_t kmeans_codes_workspace_bytes(int64_t S, int64_t E, int64_t M, int64_t K, km_dtype xt);

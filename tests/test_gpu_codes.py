@@ -304,3 +304,18 @@ def test_a_group_of_any_length(km):
         gx = km.kmeans_codes_product_grad(gy.cuda(), *args, K, scales.cuda(), group, offsets.cuda())
         ref, mag = _ref(gy, W, offsets, True)
         _close(gx, ref, mag, M, torch.bfloat16, True, f"gradient, group {group}")
+
+
+@pytest.mark.parametrize("E,M,K", [(3, 48, 64), (1, 33, 63), (4096, 16, 32), (4096, 5, 31)])
+def test_as_many_rows_as_a_call_takes(km, E, M, K):
+    S, dtype = 1 << 20, torch.bfloat16
+    lab, table, scales, offsets, W = _case(S, E, M, K, 32, dtype, "each", 50, S - 100)
+    g = torch.Generator().manual_seed(51)
+    x, gy = torch.randn((S, K), generator=g).to(dtype), torch.randn((S, M), generator=g).to(dtype)
+    args = (_packed(km, lab), table.cuda())
+    y = km.kmeans_codes_product(x.cuda(), *args, M, scales.cuda(), 32, offsets.cuda())
+    ref, mag = _ref(x, W, offsets, False)
+    _close(y, ref, mag, K, dtype, False, "product")
+    gx = km.kmeans_codes_product_grad(gy.cuda(), *args, K, scales.cuda(), 32, offsets.cuda())
+    ref, mag = _ref(gy, W, offsets, True)
+    _close(gx, ref, mag, M, dtype, True, "gradient")

@@ -121,3 +121,16 @@ def test_python_wrappers_want_gpu_tensors():
             call()
     with pytest.raises(TypeError, match="Tensor"):
         km.kmeans_lookup(None, i32)
+
+
+def test_rows_of_a_4_bit_product(lib):
+    # 2^20 rows (131072 tokens of 8 choices) pass the check of sizes, with any number of
+    # experts: the next check refuses; one more row does not
+    misaligned = C.c_void_p(0x1004)
+    for fn in (lib.kmeans_codes_product, lib.kmeans_codes_product_grad):
+        for E in (1, 4096):
+            call = _call(fn, dict(x=FAKE, xt=F16, S=1 << 20, codes=misaligned, table=FAKE, table_rows=64, scales=None,
+                                  group=0, E=E, M=64, K=128, offsets=FAKE, out=FAKE, ws=WS, ws_bytes=1 << 30,
+                                  stream=None))
+            assert call() == 1 and b"codes" in lib.kmeans_last_error()
+            assert call(S=(1 << 20) + 1) == 2 and b"2^20" in lib.kmeans_last_error()
