@@ -535,8 +535,8 @@ def kmeans_pack_codes(labels, codes=None):
 
 
 def codes_workspace(S: int, E: int, M: int, K: int, dtype: torch.dtype, device) -> torch.Tensor:
-    """A workspace for kmeans_codes_product and kmeans_codes_product_grad at
-    these shapes."""
+    """A workspace for kmeans_codes_product_grad at these shapes (the product
+    itself needs none)."""
     return _bytes(_lib.load().kmeans_codes_workspace_bytes(S, E, M, K, _DT[dtype]), device)
 
 
@@ -568,10 +568,13 @@ def _codes_call(name, x, codes, table, M, K, scales, group, offsets, out, n_out,
     elif E != 1:
         raise ValueError("offsets are needed for more than one expert")
     out = _output(out, "out", dev, dt, (S, n_out))
-    ws = codes_workspace(S, E, M, K, dt, dev) if ws is None else _tensor(ws, "workspace", dev, torch.uint8, None)
+    if ws is not None:
+        _tensor(ws, "workspace", dev, torch.uint8, None)
+    elif name == "kmeans_codes_product_grad":
+        ws = codes_workspace(S, E, M, K, dt, dev)
     st = getattr(_lib.load(), name)(x.data_ptr(), _DT[dt], S, codes.data_ptr(), table.data_ptr(), rows, _ptr(scales),
-                                    group, E, M, K, _ptr(offsets), out.data_ptr(), ws.data_ptr(), ws.numel(),
-                                    _stream(dev))
+                                    group, E, M, K, _ptr(offsets), out.data_ptr(), _ptr(ws),
+                                    0 if ws is None else ws.numel(), _stream(dev))
     if st:
         _lib.check(st, name)
     return out

@@ -334,8 +334,6 @@ __global__ __launch_bounds__(64 * WR * WK) void k_codes_product(
     }
 }
 
-size_t codes_product_scratch(int64_t, int64_t, int64_t, int64_t) { return 0; }
-
 // Groups of scales in a row (a group may be of any length: no sum with it).
 static int64_t groups_per_row(const CodesArgs& a) { return a.scales ? (a.K - 1) / a.group + 1 : 0; }
 
@@ -410,7 +408,7 @@ static hipError_t product_launch(const CodesArgs& a, hipStream_t s) {
     return hipGetLastError();
 }
 
-hipError_t launch_codes_product(DType xt, const CodesArgs& a, void*, hipStream_t s) {
+hipError_t launch_codes_product(DType xt, const CodesArgs& a, hipStream_t s) {
     if (a.S == 0 || a.M == 0) return hipSuccess;
     return xt == DType::F16 ? product_launch<_Float16>(a, s) : product_launch<__bf16>(a, s);
 }

@@ -417,9 +417,8 @@ struct CodesArgs {
     void* out;              // [S][M] (or [S][K])
     int64_t S, E, M, K, group, table_rows;
 };
-size_t codes_product_scratch(int64_t S, int64_t E, int64_t M, int64_t K);
 size_t codes_product_grad_scratch(int64_t S, int64_t E, int64_t M, int64_t K);
-hipError_t launch_codes_product(DType xt, const CodesArgs& a, void* ws, hipStream_t s);
+hipError_t launch_codes_product(DType xt, const CodesArgs& a, hipStream_t s);
 hipError_t launch_codes_product_grad(DType xt, const CodesArgs& a, void* ws, hipStream_t s);
 
 }  // namespace km

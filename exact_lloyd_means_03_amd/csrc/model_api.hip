@@ -109,12 +109,11 @@ km_status run_codes(bool grad, const void* x, int xt, int64_t S, const void* cod
     KM_TRY(need(out, S, "out"));
     if (E > 1) KM_TRY(need(offsets, S, "offsets"));
     if ((uintptr_t)codes % 16 != 0) return fail(KM_EINVAL, "codes must be 16-byte aligned");
-    const size_t n = grad ? codes_product_grad_scratch(S, E, M, K) : codes_product_scratch(S, E, M, K);
-    KM_TRY(check_ws_bytes(n, workspace, workspace_bytes));
+    if (grad) KM_TRY(check_ws_bytes(codes_product_grad_scratch(S, E, M, K), workspace, workspace_bytes));
     const CodesArgs a{x, codes, table, scales, offsets, out, S, E, M, K, group, table_rows};
     const DType t = (DType)xt;
     if (grad) KM_HIP(launch_codes_product_grad(t, a, workspace, (hipStream_t)stream), "codes_product_grad");
-    else KM_HIP(launch_codes_product(t, a, workspace, (hipStream_t)stream), "codes_product");
+    else KM_HIP(launch_codes_product(t, a, (hipStream_t)stream), "codes_product");
     return KM_OK;
 }
 
@@ -237,8 +236,7 @@ km_status kmeans_pack_codes(const int32_t* labels, int64_t M, int64_t K, void* c
 
 size_t kmeans_codes_workspace_bytes(int64_t S, int64_t E, int64_t M, int64_t K, km_dtype xt_) {
     if (check_codes(S, E, M, K, enum_code(xt_)) != KM_OK) return 0;
-    const size_t a = codes_product_scratch(S, E, M, K), b = codes_product_grad_scratch(S, E, M, K);
-    return a > b ? a : b;
+    return codes_product_grad_scratch(S, E, M, K);
 }
 
 km_status kmeans_codes_product(const void* x, km_dtype xt, int64_t S, const void* codes, const void* table,

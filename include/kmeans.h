@@ -404,9 +404,10 @@ KM_API km_status kmeans_pack_codes(const int32_t *labels, int64_t M, int64_t K, 
  *   offsets  [E+1] int32, ascending from 0, offsets[E] <= S; NULL with E == 1
  *            means all S rows.
  *   out      [S,M] (grad: [S,K]) of dtype xt.
- * S, M, K <= 2^20, E <= 4096.  The workspace must hold
+ * S, M, K <= 2^20, E <= 4096.  The gradient's workspace must hold
  * kmeans_codes_workspace_bytes(S, E, M, K, xt) bytes, 256-byte aligned (0
- * from the query: none is needed, or the shapes are invalid). */
+ * from the query: none is needed, or the shapes are invalid).  The product
+ * needs none and does not look at the one it is given (NULL is fine). */
 KM_API size_t kmeans_codes_workspace_bytes(int64_t S, int64_t E, int64_t M, int64_t K, km_dtype xt);
 KM_API km_status kmeans_codes_product(const void *x, km_dtype xt, int64_t S, const void *codes, const void *table,
                                int64_t table_rows, const void *scales, int64_t group, int64_t E, int64_t M,

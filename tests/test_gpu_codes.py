@@ -319,3 +319,20 @@ def test_as_many_rows_as_a_call_takes(km, E, M, K):
     gx = km.kmeans_codes_product_grad(gy.cuda(), *args, K, scales.cuda(), 32, offsets.cuda())
     ref, mag = _ref(gy, W, offsets, True)
     _close(gx, ref, mag, M, dtype, True, "gradient")
+
+
+def test_the_product_takes_no_workspace(km):
+    # a shape whose gradient adds 16 MB of partial sums
+    S, M, K = 256, 4096, 4096
+    codes = torch.zeros((M // 16, K // 128, 1024), dtype=torch.uint8, device="cuda")
+    table = torch.ones((M, 16), dtype=torch.bfloat16, device="cuda")
+    x = torch.ones((S, K), dtype=torch.bfloat16, device="cuda")
+    assert km.codes_workspace(S, 1, M, K, x.dtype, "cuda").numel() >= 1 << 24
+    out = torch.empty((S, M), dtype=x.dtype, device="cuda")
+    torch.cuda.synchronize()
+    torch.cuda.reset_peak_memory_stats()
+    before = torch.cuda.memory_allocated()
+    km.kmeans_codes_product(x, codes, table, M, out=out)
+    assert torch.cuda.max_memory_allocated() == before
+    assert (out == K).all()
+    km.kmeans_codes_product(x, codes, table, M, out=out, ws=torch.empty(1, dtype=torch.uint8, device="cuda"))
