@@ -378,7 +378,15 @@ hipError_t launch_lookup(DType xt, const void* table, int64_t B, int64_t V, int6
 // blocks each read M labels.  Against the counting pass and the copy, us a
 // call: T x M of 2^20 (1024 x 1024) 8.9 and 15.4, 2^21 (1024 x 2048) 11.5 and
 // 15.6, (512 x 4096) 15.7 and 15.4, 2^22 (2048 x 2048) 18.5 and 15.9.
-inline bool dispatch_small(int64_t T, int64_t M) { return M <= 4096 && T * M <= (int64_t)1 << 21; }
+// A block takes eight choices of its token at a time, each time reading the
+// labels and the row again, so more choices leave room for fewer labels (rows of
+// 512 and of 8192 bytes, against 17 us): top 16, M 1024 12.9 and 16.4, M 4096
+// 25.6 and 30.8; top 17, M 272 13.1 and 16.2, M 1088 17.9 and 21.9; top 32, M 32
+// 16.2 and 21.5; top 64, M 64 30.7 and 40.8 (20 and 23).
+inline bool dispatch_small(int64_t T, int64_t top) {
+    const int64_t M = T * top, passes = (top + 7) / 8;
+    return M <= (passes <= 3 ? 4096 >> 2 * (passes - 1) : 0) && T * M <= (int64_t)1 << 21;
+}
 hipError_t launch_dispatch_small(DType xt, const void* x, int64_t T, int64_t d, int64_t top, const int32_t* experts,
                                  int64_t E, void* rows, int32_t* offsets, int32_t* slots, int32_t* order,
                                  hipStream_t s);

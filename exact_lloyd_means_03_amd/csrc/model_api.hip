@@ -69,7 +69,7 @@ struct DispatchPlan {
 DispatchPlan plan_dispatch(int64_t T, int64_t top, int64_t E) {
     DispatchPlan p;
     const int64_t M = T * top;
-    if (dispatch_small(T, M)) return p;
+    if (dispatch_small(T, top)) return p;
     const size_t rows = align_up((size_t)rank_chunks(1, M) * E * sizeof(int32_t));
     p.prefix = rows;
     p.counts = 2 * rows;
@@ -178,7 +178,7 @@ km_status kmeans_dispatch(const void* x, km_dtype xt_, int64_t T, int64_t d, con
     const DispatchPlan p = plan_dispatch(T, top, E);
     KM_TRY(check_ws_bytes(p.total, workspace, workspace_bytes));
     hipStream_t s = (hipStream_t)stream;
-    if (dispatch_small(T, M)) {
+    if (dispatch_small(T, top)) {
         KM_HIP(launch_dispatch_small((DType)xt, x, T, d, top, experts, E, rows, offsets, slots, order, s), "dispatch");
         return KM_OK;
     }

@@ -134,3 +134,10 @@ def test_rows_of_a_4_bit_product(lib):
                                   stream=None))
             assert call() == 1 and b"codes" in lib.kmeans_last_error()
             assert call(S=(1 << 20) + 1) == 2 and b"2^20" in lib.kmeans_last_error()
+
+
+def test_many_choices_are_sorted_in_passes_of_their_own(lib):
+    # (no workspace: one launch, whose blocks read every label once for eight choices)
+    q = lib.kmeans_dispatch_workspace_bytes
+    assert q(512, 8, 64) == 0 and q(64, 16, 64) == 0 and q(8, 24, 64) == 0 and q(0, 4096, 8) == 0
+    assert q(256, 16, 64) > 0 and q(64, 17, 64) > 0 and q(1, 64, 64) > 0 and q(1, 4096, 256) > 0
