@@ -1,4 +1,5 @@
-"""Python entry points with the C ABI's names (argument marshalling only).
+"""Python entry points with the C ABI's names (argument marshalling, and the
+operators' gradients handed to torch's autograd).
 
 Tensors are torch tensors on the GPU: torch provides the device memory and
 the stream (the current stream of the tensors' device).  Every step of the
@@ -386,13 +387,27 @@ def _output(t, name, dev, dtype, shape):
     return torch.empty(shape, dtype=dtype, device=dev) if t is None else _tensor(t, name, dev, dtype, shape)
 
 
+def _no_gradient(name, **tensors):
+    # a result without history would lose these tensors' gradients without a word
+    for arg, t in tensors.items():
+        if t is not None and t.requires_grad and torch.is_grad_enabled():
+            raise ValueError(f"{name} has no gradient of {arg}: pass {arg}.detach(), or call it under torch.no_grad()")
+
+
+def _no_buffers(name, *buffers):
+    if any(b is not None for b in buffers):
+        raise ValueError(f"{name} cannot write to given tensors where autograd records it: pass none, or call it "
+                         "under torch.no_grad()")
+
+
 def _bytes(n, device):
     return torch.empty(max(int(n), 256), dtype=torch.uint8, device=device)
 
 
 def kmeans_lookup(table, labels, scale: float = 1.0, out=None):
     """scale * table[b, labels[b, i]] for every label: table [B, V, d], labels
-    [B, N] int32 -> [B, N, d]; labels outside [0, V) give rows of zeros."""
+    [B, N] int32 -> [B, N, d]; labels outside [0, V) give rows of zeros.
+    Differentiable in table."""
     _tensor(table, "table", None, None, None)
     if table.dim() != 3:
         raise ValueError("table must be [B, V, d]")
@@ -401,6 +416,9 @@ def kmeans_lookup(table, labels, scale: float = 1.0, out=None):
     _tensor(labels, "labels", dev, torch.int32, None)
     if labels.dim() != 2 or labels.shape[0] != B:
         raise ValueError("labels must be [B, N] int32")
+    if table.requires_grad and torch.is_grad_enabled():
+        _no_buffers("kmeans_lookup", out)
+        return _Lookup.apply(table, labels, scale)
     N = labels.shape[1]
     out = _output(out, "out", dev, table.dtype, (B, N, d))
     st = _lib.load().kmeans_lookup(table.data_ptr(), _DT[table.dtype], B, V, d, labels.data_ptr(), N, scale,
@@ -422,6 +440,8 @@ def kmeans_lookup_grad(grad, labels, V: int, scale: float = 1.0, out=None, ws=No
     _tensor(grad, "grad", None, None, None)
     if grad.dim() != 3:
         raise ValueError("grad must be [B, N, d]")
+    if grad.requires_grad:
+        _no_gradient("kmeans_lookup_grad", grad=grad)
     B, N, d = grad.shape
     dev = grad.device
     _tensor(labels, "labels", dev, torch.int32, (B, N))
@@ -449,8 +469,8 @@ def kmeans_dispatch(x, experts, E: int, rows=None, plan=None, ws=None):
     [T, top], order [T * top]): expert e's rows are rows[offsets[e] :
     offsets[e + 1]], rows[slots[t, k]] = x[t], order[p] = t * top + k, and the
     rows from offsets[E] on are zeros with order -1; dropped choices have slot
-    -1.  plan: (offsets, slots, order) tensors to write.  The gradient of x is
-    kmeans_combine(grad_rows, slots, None)."""
+    -1.  plan: (offsets, slots, order) tensors to write.  Differentiable in x;
+    its gradient is kmeans_combine(grad_rows, slots, None)."""
     _tensor(x, "x", None, None, None)
     if x.dim() != 2:
         raise ValueError("x must be [T, d]")
@@ -459,6 +479,9 @@ def kmeans_dispatch(x, experts, E: int, rows=None, plan=None, ws=None):
     _tensor(experts, "experts", dev, torch.int32, None)
     if experts.dim() != 2 or experts.shape[0] != T:
         raise ValueError("experts must be [T, top] int32")
+    if x.requires_grad and torch.is_grad_enabled():
+        _no_buffers("kmeans_dispatch", rows, plan)
+        return _Dispatch.apply(x, experts, E, ws)
     top = experts.shape[1]
     rows = _output(rows, "rows", dev, x.dtype, (T * top, d))
     offsets, slots, order = (None, None, None) if plan is None else plan
@@ -488,10 +511,14 @@ def _sorted_rows(rows, slots):
 
 def kmeans_combine(rows, slots, weights=None, out=None):
     """Sorted rows back at their tokens: out[t] = sum_k weights[t, k] *
-    rows[slots[t, k]] (weights None: all 1), slots -1 adding nothing."""
+    rows[slots[t, k]] (weights None: all 1), slots -1 adding nothing.
+    Differentiable in rows and weights."""
     T, top, d, dev = _sorted_rows(rows, slots)
     if weights is not None:
         _tensor(weights, "weights", dev, torch.float32, (T, top))
+    if (rows.requires_grad or weights is not None and weights.requires_grad) and torch.is_grad_enabled():
+        _no_buffers("kmeans_combine", out)
+        return _Combine.apply(rows, slots, weights)
     out = _output(out, "out", dev, rows.dtype, (T, d))
     st = _lib.load().kmeans_combine(rows.data_ptr(), _DT[rows.dtype], T, d, top, slots.data_ptr(), _ptr(weights),
                                     out.data_ptr(), _stream(dev))
@@ -508,6 +535,8 @@ def kmeans_combine_grad(grad, rows, slots, order, weights, grad_rows=None, grad_
     _tensor(grad, "grad", dev, rows.dtype, (T, d))
     _tensor(order, "order", dev, torch.int32, (T * top,))
     _tensor(weights, "weights", dev, torch.float32, (T, top))
+    if grad.requires_grad or rows.requires_grad or weights.requires_grad:
+        _no_gradient("kmeans_combine_grad", grad=grad, rows=rows, weights=weights)
     grad_rows = _output(grad_rows, "grad_rows", dev, rows.dtype, (T * top, d))
     grad_weights = _output(grad_weights, "grad_weights", dev, torch.float32, (T, top))
     st = _lib.load().kmeans_combine_grad(grad.data_ptr(), rows.data_ptr(), _DT[rows.dtype], T, d, top,
@@ -567,6 +596,13 @@ def _codes_call(name, x, codes, table, M, K, scales, group, offsets, out, n_out,
         _tensor(offsets, "offsets", dev, torch.int32, (E + 1,))
     elif E != 1:
         raise ValueError("offsets are needed for more than one expert")
+    if x.requires_grad or table.requires_grad or (scales is not None and scales.requires_grad):
+        _no_gradient(name, table=table, scales=scales)
+        if name == "kmeans_codes_product_grad":
+            _no_gradient(name, grad=x)
+        elif x.requires_grad and torch.is_grad_enabled():
+            _no_buffers(name, out)
+            return _Product.apply(x, codes, table, M, scales, group, offsets)
     out = _output(out, "out", dev, dt, (S, n_out))
     if ws is not None:
         _tensor(ws, "workspace", dev, torch.uint8, None)
@@ -586,7 +622,8 @@ def kmeans_codes_product(x, codes, table, M: int, scales=None, group: int = 0, o
     offsets[e] : offsets[e + 1] holds p (offsets None: one matrix).  x [S, K]
     float16 / bfloat16, codes of kmeans_pack_codes (stacked over the experts),
     table [E, M, 16] or [E, 1, 16] and scales [E, M, ceil(K / group)] of x's
-    dtype.  Returns [S, M]; rows past offsets[E] are zeros."""
+    dtype.  Returns [S, M]; rows past offsets[E] are zeros.  Differentiable in
+    x; the codebooks and scales are held."""
     _tensor(x, "x", None, None, None)
     if x.dim() != 2:
         raise ValueError("x must be [S, K]")
@@ -600,3 +637,69 @@ def kmeans_codes_product_grad(grad, codes, table, K: int, scales=None, group: in
         raise ValueError("grad must be [S, M]")
     return _codes_call("kmeans_codes_product_grad", grad, codes, table, grad.shape[1], K, scales, group, offsets, out,
                        K, ws)
+
+
+# What autograd records of a call whose input requires a gradient: the call
+# itself and, backwards, the entry point of its gradient.  (forward runs with
+# recording off.)
+
+class _Lookup(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, table, labels, scale):
+        ctx.save_for_backward(labels)
+        ctx.V, ctx.scale = table.shape[1], scale
+        return kmeans_lookup(table, labels, scale)
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, grad):
+        return kmeans_lookup_grad(grad.contiguous(), ctx.saved_tensors[0], ctx.V, ctx.scale), None, None
+
+
+class _Dispatch(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, experts, E, ws):
+        rows, *plan = kmeans_dispatch(x, experts, E, ws=ws)
+        ctx.mark_non_differentiable(*plan)
+        ctx.save_for_backward(plan[1])
+        return (rows, *plan)
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, grad, *_):
+        return kmeans_combine(grad.contiguous(), ctx.saved_tensors[0], None), None, None, None
+
+
+class _Combine(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, rows, slots, weights):
+        ctx.save_for_backward(rows, slots, weights)
+        return kmeans_combine(rows, slots, weights)
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, grad):
+        rows, slots, weights = ctx.saved_tensors
+        S = slots.numel()
+        # the dispatch's order, of which the gradient reads where it is -1
+        flat = slots.view(-1)
+        order = torch.full((S + 1,), -1, dtype=torch.int32, device=slots.device)
+        order.index_fill_(0, torch.where((flat >= 0) & (flat < S), flat, S).long(), 0)
+        ones = torch.ones(slots.shape, device=slots.device) if weights is None else weights
+        grad_rows, grad_weights = kmeans_combine_grad(grad.contiguous(), rows, slots, order[:S], ones)
+        return grad_rows, None, None if weights is None else grad_weights
+
+
+class _Product(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, codes, table, M, scales, group, offsets):
+        ctx.save_for_backward(codes, table, scales, offsets)
+        ctx.K, ctx.group = x.shape[1], group
+        return kmeans_codes_product(x, codes, table, M, scales, group, offsets)
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, grad):
+        codes, table, scales, offsets = ctx.saved_tensors
+        return (kmeans_codes_product_grad(grad.contiguous(), codes, table, ctx.K, scales, ctx.group, offsets),
+                *[None] * 6)
