@@ -8,10 +8,12 @@
 namespace km {
 
 // labels [M][K] -> tiles (layout in include/kmeans.h).  One thread per 32-bit
-// word: 16 bytes per lane and tile, consecutive lanes consecutive words.
+// word: 16 bytes per lane and tile, consecutive lanes consecutive words.  Done
+// once for a matrix: 4096 x 4096 in 36 us, 2.1 TB/s; eight single loads with a
+// bound check each are what it waits for.
 __global__ __launch_bounds__(256) void k_pack_codes(const int32_t* __restrict__ labels, int64_t M, int64_t K,
                                                     int64_t KT, int64_t words, uint32_t* __restrict__ codes,
-                                                   int64_t block0) {
+                                                    int64_t block0) {
     const int64_t i = (block0 + blockIdx.x) * 256 + threadIdx.x;
     if (i >= words) return;
     const int64_t tile = i >> 8;
@@ -128,8 +130,11 @@ __device__ __forceinline__ void store4(uint16_t* __restrict__ to, int64_t n, f32
 // One row by 4096 x 4096 (f16, groups of 128): 6.4 us, a block's chain of
 // loads; 64 rows over 16 experts of 4096 x 2048: 24 us for 73 MB (3.0 TB/s),
 // vector instructions (decoding) issue 74% of the time; 4096 rows over 8
-// experts of 4096 x 4096: 198 us (695 TFLOP/s), matrix cores 38% and vector
-// instructions 62% of the cycles; with experts of equal size 165-182 us.
+// experts of 4096 x 4096: 201 us in a stream of calls (684 TFLOP/s; the first
+// hundred launches on an idle device 221 us), matrix cores 37%, vector instructions 61% and LDS reads 20% of the cycles.
+// 1155 blocks on 512 places (252 registers, 66 KB of LDS) make three rounds, the
+// last a quarter full, and an eighth of the token tiles is padding; with experts
+// of equal size, two full rounds, it takes 168-172 us.
 enum { kXNone, kXDirect, kXCopy };
 
 template <int WR, int WK, int U, int R, int NT, int GS, int X>
@@ -355,7 +360,21 @@ static int groups_per_tile(const CodesArgs& a) {
 //     64, 8 of those      29.1      27.9     29.7      31.6      38.3       63.0
 //    512, 8 of those      97.4      74.5     54.2      47.6      39.5       63.5
 //   2048, 8 of those     354.2     261.2    189.5     164.6     119.6       93.3
-// (tokens x rows of a block).
+// (tokens x rows of a block).  Rows that are no multiple of 8 columns are copied
+// through registers and have three of the blocks, which take half again to four
+// times as long (K = 4097, us a call; the last column: what the rule takes at
+// K = 4096):
+//   tokens, matrices   16 x 16  32 x 128  128 x 128   K = 4096
+//     16, 4096 x 4097      9.6      33.6       85.4        8.1
+//     64, 4096 x 4097     25.6      36.7       93.3       14.1
+//    256, 4096 x 4097     93.5      39.6      113.2       26.8
+//   1024, 4096 x 4097    391.9     159.6      154.4       59.9
+//   2048, 4096 x 4097    780.1     317.0      174.8       86.3
+//     64, 8 of those      58.1      42.8       93.6       26.3
+//    512, 8 of those     215.4      85.0      120.9       36.3
+//   2048, 8 of those     839.6     318.5      176.2       88.2
+// (the rule takes the fastest but at 16 to 128 tokens over 8 matrices, where the
+// first stays up to 1.4 times the second).
 template <typename T>
 static hipError_t product_launch(const CodesArgs& a, hipStream_t s) {
     const int64_t MT = code_tiles_m(a.M), KT = code_tiles_k(a.K);
@@ -431,17 +450,19 @@ hipError_t launch_codes_product(DType xt, const CodesArgs& a, hipStream_t s) {
 // float32 sum.  float16 lacks the range of a product of two of its numbers, so
 // weights are held there times 2^13, and a step that has any outside 2^-27 .. 4
 // takes its weights in three passes, each with a power of two of its own
-// (Half<_Float16>, codes.h).  Looking for such weights costs float16 8% of the
-// kernel's time (2048 tokens over 8 experts of 4096 x 2048: 99 us, bfloat16 93).
+// (Half<_Float16>, codes.h).  Looking for such weights costs float16 5 to 8% of
+// the time (2048 tokens over 8 experts of 4096 x 2048: 98 us, 92 without it);
+// where every step has some, the call takes 460 us.
 //
 // Few tokens: the rows are split over blockIdx.z and the float32 partial sums
 // added in order by k_codes_grad_join.
 //
-// 2048 tokens over 8 experts of 4096 x 2048 (bf16, groups of 64): 105 us, 330
-// TFLOP/s; matrix cores 30% of the cycles, vector instructions 42%, waiting at
+// 2048 tokens over 8 experts of 4096 x 2048 (bf16, groups of 64): 95 us in a
+// stream of calls, 360 TFLOP/s (105 us for the first hundred launches on an idle
+// device); matrix cores 30% of the cycles, vector instructions 42%, waiting at
 // the step's barrier and for LDS most of the rest.  A step moves about 200 KB
-// through LDS for 4 MFLOP; tokens loaded straight to operands instead (148 us)
-// and half the waves a phase apart (125 us) were slower.
+// through LDS for 4 MFLOP; tokens loaded straight to operands instead (148 us,
+// against 106 then) and half the waves a phase apart (125 us) were slower.
 constexpr int kGradWaves = 8, kGradRows = 64;
 
 // 16-byte chunk of row m that holds columns 8 c .. 8 c + 7.  The 16 rows that
@@ -520,7 +541,7 @@ __global__ __launch_bounds__(64 * kGradWaves) void k_codes_grad(
                         whole ? load8(p) : load8_end(p, (int)(M - m0) - c * 8);
                 }
             }
-            // slots 0-3: codes of a row tile; 4, 5: 32 codebooks; 6 + h: scales; the rest repeat slot 0
+            // waves 0-3: the codes of a row tile each; 4, 5: 32 codebooks each; the scales below
             auto codes_of = [&](int i) {
                 const int64_t mt = st * (kGradRows / 16) + i;
                 dma16(ct + (mt < MT ? mt : MT - 1) * KT * kCodeTile, lane * 16, to.codes + i * kCodeTile);
@@ -703,8 +724,23 @@ __global__ __launch_bounds__(256) void k_codes_grad_join(const float* __restrict
 
 // Tokens of a block (64 ntw) and splits of the rows, by the time they take:
 // steps of a block one after the other, in rounds of 256 blocks (one for each
-// compute unit), and the partial sums' way through memory.  Measured: a step
-// of 64, 128, 256 tokens takes about 1.07, 1.26 and 1.47 us.
+// compute unit), and the partial sums' way through memory.  step_us are a first
+// kernel's; measured since, from 4096 and 8192 rows by 256 blocks (bf16 and f16,
+// groups of 64 and 128): a step of 64, 128, 256 tokens takes 0.93-0.98, 1.06-1.11
+// and 1.28-1.36 us, the same ratios within 5%, and 3-14 us come on top.
+// us a call, bf16, groups of 128 (64 ntw tokens / splits; the last column: the
+// rule's choice):
+//   tokens, matrices    64/1   64/4  64/16  128/1  128/4  256/1  256/4   rule
+//     16, 4096 x 4096   65.7   22.5   17.5   71.6   24.5   85.7   28.8   16.2
+//    256, 4096 x 4096   67.4   35.5   48.8   73.2   31.5   88.1   35.7   30.1
+//    512, 4096 x 4096   69.5   59.9   88.9   78.6   55.4   90.8   41.2   38.7
+//   1024, 4096 x 4096   93.5  111.0  180.4   80.0  102.2   92.2   72.5   61.0
+//   2048, 4096 x 4096  180.3  213.5  400.9  157.2  198.8   94.4  135.9   94.5
+//     64, 8 4096 x 2048 67.7   32.7   43.6   77.1   48.7   91.5   57.4   50.4
+//    512, 8 4096 x 2048 69.0   38.6   59.2   79.2   53.2   93.4   61.7   47.0
+//   2048, 8 4096 x 2048 94.7  115.5  207.3   81.7  107.9   94.7   76.8   94.9
+// It misses where two blocks of 64 or 128 tokens share a compute unit, which it
+// counts as two rounds (the last three lines).
 struct GradShape {
     int ntw;
     int64_t splits;

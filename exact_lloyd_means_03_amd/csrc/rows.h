@@ -59,11 +59,12 @@ __device__ __forceinline__ typename RowVec<T>::V load_raw(const T* __restrict__ 
     return v;
 }
 
-// STREAM: a non-temporal store.  Results too large for the memory-side cache
-// (256 MB) are not found there by whoever reads them next; kept out of it, they
-// neither evict the operator's inputs nor have to be written back while the
-// next launch reads (lookup of 49999 rows of 8 KB: 112 -> 82 us; dispatch and
-// combine of 98526 rows of 4 KB: 74 + 128 -> 85 + 87 us).
+// STREAM: a non-temporal store, for results of half the memory-side cache's
+// 256 MB or more: with the inputs beside them they would not all be found there
+// by whoever reads them next; kept out of it, they neither evict the operator's
+// inputs nor have to be written back while the next launch reads (lookup of
+// 49999 rows of 8 KB: 112 -> 82 us; dispatch and combine of 98526 rows of 4 KB:
+// 74 + 128 -> 85 + 87 us).
 inline bool stream_out(int64_t bytes) { return bytes >= ((int64_t)128 << 20); }
 template <typename T, bool STREAM = false>
 __device__ __forceinline__ void store_raw(T* __restrict__ p, int d, typename RowVec<T>::V v) {
