@@ -740,7 +740,8 @@ __global__ __launch_bounds__(256) void k_codes_grad_join(const float* __restrict
 //    512, 8 4096 x 2048 69.0   38.6   59.2   79.2   53.2   93.4   61.7   47.0
 //   2048, 8 4096 x 2048 94.7  115.5  207.3   81.7  107.9   94.7   76.8   94.9
 // It misses where two blocks of 64 or 128 tokens share a compute unit, which it
-// counts as two rounds (the last three lines).
+// counts as two rounds, and where experts of equal size fill their tiles, of
+// which it expects half a tile more for each (the last three lines).
 struct GradShape {
     int ntw;
     int64_t splits;
