@@ -51,6 +51,19 @@ SIGNATURES = {
                                        _p]),
     "kmeans_codes_product_grad": (C.c_int, [_p, C.c_int, _i64, _p, _p, _i64, _p, _i64, _i64, _i64, _i64, _p, _p, _p,
                                             _sz, _p]),
+    "kmeans_quantize": (C.c_int, [_p, C.c_int, _i64, _i64, _i64, _i64, _p, _p, _p]),
+    "kmeans_norm": (C.c_int, [_p, C.c_int, _i64, _i64, _p, _p, C.c_int, C.c_float, _p, _p, _p, _p, _p]),
+    "kmeans_norm_grad_workspace_bytes": (_sz, [_i64, _i64, C.c_int]),
+    "kmeans_norm_grad": (C.c_int, [_p, _p, C.c_int, _i64, _i64, _p, _p, C.c_int, C.c_float, _p, _p, _p, _sz, _p]),
+    "kmeans_gate_workspace_bytes": (_sz, [_i64, _i64]),
+    "kmeans_gate": (C.c_int, [_p, C.c_int, _i64, _i64, _i64, _i32, _p, _p, _p, _p, _p, _p, _sz, _p]),
+    "kmeans_gate_grad": (C.c_int, [_p, C.c_int, _i64, _i64, _i64, _i32, _p, _p, _p, _p, _p, _p]),
+    "kmeans_plan_workspace_bytes": (_sz, [_i64, _i64, _i64]),
+    "kmeans_plan": (C.c_int, [_p, _i64, _i64, _i64, _p, _p, _p, _p, _sz, _p]),
+    "kmeans_block_product_workspace_bytes": (_sz, [_i64, _i64, _i64, _i64]),
+    "kmeans_block_product": (C.c_int, [_p, _p, _i64, _p, _p, _i64, _i64, _i64, _p, _p, _i64, _p, C.c_int, _p, _sz, _p]),
+    "kmeans_block_product_grad_workspace_bytes": (_sz, [_i64, _i64, _i64, _i64]),
+    "kmeans_block_product_grad": (C.c_int, [_p, _p, _i64, _p, _p, _i64, _i64, _i64, _p, _p, C.c_int, _p, _sz, _p]),
     "kmeans_status_str": (C.c_char_p, [C.c_int]),
     "kmeans_last_error": (C.c_char_p, []),
     "kmeans_version": (C.c_int, []),

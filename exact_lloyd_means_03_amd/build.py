@@ -25,7 +25,8 @@ SAN_FLAGS = ["-Xarch_host", "-fsanitize=address", "-Xarch_host", "-fsanitize=und
              "-Xarch_host", "-fno-omit-frame-pointer", "-Xarch_host", "-fno-sanitize-recover=undefined"]
 
 SOURCES = ["small.hip", "assign_mfma.hip", "assign_1d.hip", "fit_1d.hip", "optimal_1d.hip", "emeans.hip",
-           "sort.hip", "update.hip", "api.hip", "rows.hip", "label_rank.hip", "lookup_grad.hip", "codes.hip", "model_api.hip"]
+           "sort.hip", "update.hip", "api.hip", "rows.hip", "label_rank.hip", "lookup_grad.hip", "codes.hip", "model_api.hip",
+           "norm.hip", "gate.hip", "block_product.hip", "layer_api.hip"]
 
 CFLAGS = [
     "-O3", "-std=c++17", "-fPIC", f"--offload-arch={ARCH}",

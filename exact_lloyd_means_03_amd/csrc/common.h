@@ -429,4 +429,37 @@ size_t codes_product_grad_scratch(int64_t S, int64_t E, int64_t M, int64_t K);
 hipError_t launch_codes_product(DType xt, const CodesArgs& a, hipStream_t s);
 hipError_t launch_codes_product_grad(DType xt, const CodesArgs& a, void* ws, hipStream_t s);
 
+// A layer of 8-bit experts: norms and codes (norm.hip), the gate (gate.hip),
+// products (block_product.hip).
+bool norm_fits(int64_t d, DType xt);
+hipError_t launch_norm(DType xt, const void* x, int64_t T, int64_t d, const void* residual, const void* weight, DType wt,
+                       float eps, void* h, void* y, void* codes, float* scales, hipStream_t s);
+size_t norm_grad_scratch(int64_t T, int64_t d, DType xt);
+hipError_t launch_norm_grad(DType xt, const void* grad, const void* h, int64_t T, int64_t d, const void* gres,
+                            const void* weight, DType wt, float eps, void* gx, void* gw, void* ws, hipStream_t s);
+hipError_t launch_quantize(DType xt, const void* x, int64_t B, int64_t M, int64_t K, bool matrix, void* codes,
+                           float* scales, hipStream_t s);
+bool gate_top_fits(int64_t top);
+size_t gate_scratch(int64_t T, int64_t E);
+hipError_t launch_gate(DType xt, const void* logits, int64_t T, int64_t E, int64_t top, bool normalize, int32_t* experts,
+                       float* weights, int32_t* counts, float* shares, float* loss, void* ws, hipStream_t s);
+hipError_t launch_gate_grad(DType xt, const void* logits, int64_t T, int64_t E, int64_t top, bool normalize,
+                            const int32_t* experts, const int32_t* counts, const float* gweights, const float* gloss,
+                            void* out, hipStream_t s);
+// order[p] = -1 from *n on, for a plan whose rows are not copied.
+hipError_t launch_plan_tail(const int32_t* n, int64_t M, int32_t* order, hipStream_t s);
+struct BlockArgs {
+    const void* x;           // [S or T][inner] codes
+    const float* x_scales;   // [S or T][blocks of inner]
+    const void* codes;       // [E][M][K]
+    const float* scales;     // [E][blocks of M][blocks of K]
+    const int32_t* offsets;  // [E + 1] or NULL (E == 1: all rows)
+    const int32_t* order;    // [S] or NULL: row p is x's row order[p] / top
+    void* out;               // [S][outer]
+    int64_t S, E, M, K, top;
+};
+size_t block_product_scratch(int64_t S, int64_t E, int64_t M, int64_t K);
+size_t block_product_grad_scratch(int64_t S, int64_t E, int64_t M, int64_t K);
+hipError_t launch_block_product(DType ot, bool grad, const BlockArgs& a, void* ws, hipStream_t s);
+
 }  // namespace km

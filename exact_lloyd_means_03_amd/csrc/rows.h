@@ -96,12 +96,13 @@ __device__ __forceinline__ void store_f32(T* __restrict__ p, int d, const float 
 
 // A launch has fewer than 2^32 threads (hipLaunchKernel's limit in a dimension
 // of the grid): more blocks than kLaunchBlocks of 256 threads are launched in
-// parts, launch(first block, blocks).
+// parts, launch(first block, blocks); blocks of up to 64 `waves` threads where
+// waves is above 4.
 constexpr int64_t kLaunchBlocks = (int64_t)1 << 22;
 template <typename F>
-inline void in_launches(int64_t blocks, F launch) {
-    for (int64_t b0 = 0; b0 < blocks; b0 += kLaunchBlocks)
-        launch(b0, (unsigned)(blocks - b0 < kLaunchBlocks ? blocks - b0 : kLaunchBlocks));
+inline void in_launches(int64_t blocks, F launch, int waves = 4) {
+    const int64_t most = waves > 4 ? kLaunchBlocks * 4 / waves : kLaunchBlocks;
+    for (int64_t b0 = 0; b0 < blocks; b0 += most) launch(b0, (unsigned)(blocks - b0 < most ? blocks - b0 : most));
 }
 
 // Items (row, chunk) of a launch are numbered row-major; block b of threads

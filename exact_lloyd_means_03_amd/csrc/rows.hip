@@ -255,6 +255,18 @@ hipError_t launch_dispatch_small(DType xt, const void* x, int64_t T, int64_t d, 
     return hipGetLastError();
 }
 
+__global__ __launch_bounds__(kRowThreads) void k_plan_tail(const int32_t* __restrict__ n, int64_t M,
+                                                           int32_t* __restrict__ order) {
+    const int64_t p = (int64_t)blockIdx.x * kRowThreads + threadIdx.x;
+    if (p < M && p >= *n) order[p] = -1;
+}
+
+hipError_t launch_plan_tail(const int32_t* n, int64_t M, int32_t* order, hipStream_t s) {
+    hipLaunchKernelGGL(k_plan_tail, dim3((unsigned)((M + kRowThreads - 1) / kRowThreads)), dim3(kRowThreads), 0, s, n, M,
+                       order);
+    return hipGetLastError();
+}
+
 // out[t] = sum_k w[t][k] rows[slots[t][k]] (w NULL: all 1), summed in float32
 // in the order of k and rounded once; a choice without a slot adds nothing.
 // U rows are in flight per thread.  6 x 16421 rows of 4 KB: 93 us, 470 MB at

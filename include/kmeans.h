@@ -418,6 +418,148 @@ KM_API km_status kmeans_codes_product_grad(const void *grad, km_dtype xt, int64_
                                     int64_t E, int64_t M, int64_t K, const int32_t *offsets, void *out,
                                     void *workspace, size_t workspace_bytes, km_stream stream);
 
+/* ---------------------------------------------------------------------------
+ * A layer of 8-bit experts.
+ *
+ * What stands around the sorted rows above: the norm that produces a token's
+ * 8-bit row, the gate that chooses its experts, the plan of the sort alone, and
+ * products with 8-bit matrices.  The conventions of the part above hold.  Codes
+ * are 8-bit floating point numbers of the OCP format e4m3 (largest value 448,
+ * no infinities) in blocks that share a float32 scale; the value of a code is
+ * code * scale.
+ */
+
+/* 8-bit codes of a matrix by blocks of `rows` x 128 elements.
+ *   scale = max(amax / 448, 2^-100), amax the block's largest magnitude,
+ *   code  = x / scale, rounded to nearest even (from its float32 quotient).
+ * A block that holds an infinity or a NaN has values that are all NaN.
+ *   x       [B,M,K] of dtype xt.
+ *   rows    1 (rows of a product) or 128 (its matrices).
+ *   codes   out [B,M,K] bytes.
+ *   scales  out [B,ceil(M/rows),ceil(K/128)] float32.
+ * B <= 65535; M < 2^31 where rows is 1, 2^20 where it is 128; K <= 2^20. */
+KM_API km_status kmeans_quantize(const void *x, km_dtype xt, int64_t B, int64_t M, int64_t K, int64_t rows, void *codes,
+                          float *scales, km_stream stream);
+
+/* Root-mean-square norm of rows, with the residual's addition.
+ *   h[t]    = x[t] + residual[t]      (rounded once, for the output h)
+ *   y[t][j] = h[t][j] * weight[j] / sqrt(mean_j h[t][j]^2 + eps)
+ * from the unrounded float32 sum h; rounded once.
+ *   x         [T,d] of dtype xt.
+ *   residual  [T,d] of dtype xt, or NULL (h is x; the output h is not written).
+ *   weight    [d] of dtype wt: xt or KM_F32; NULL: all 1.
+ *   h         out [T,d] of dtype xt, or NULL.
+ *   y         out [T,d] of dtype xt, or NULL.
+ *   codes, scales  out [T,d] bytes and [T,ceil(d/128)] float32, or NULL both:
+ *             y as 8-bit codes by blocks of 128 columns (from the float32 y).
+ * Exactly one of y and codes is given.  Rows of at most 64 KB; eps >= 0.  A
+ * row of zeros with eps 0 is 0 / 0: NaN. */
+KM_API km_status kmeans_norm(const void *x, km_dtype xt, int64_t T, int64_t d, const void *residual, const void *weight,
+                      km_dtype wt, float eps, void *h, void *y, void *codes, float *scales, km_stream stream);
+
+/* Gradients of kmeans_norm at h, for a gradient of y (of the codes' values,
+ * where the forward call wrote codes: rounding is passed through):
+ *   r = 1 / sqrt(mean h^2 + eps), u = grad * weight,
+ *   grad_x[t]      = r u - h r^3 mean(u h) + grad_residual[t]  (rounded once)
+ *   grad_weight[j] = sum_t grad[t][j] h[t][j] r[t]
+ * grad_x is the gradient of x and of the residual.
+ *   grad, h        [T,d] of dtype xt (h as the forward call wrote it).
+ *   grad_residual  [T,d] of dtype xt or NULL: the gradient that comes to h.
+ *   grad_x         out [T,d] of dtype xt.
+ *   grad_weight    out [d] of dtype wt, or NULL: summed in float32, in an order
+ *                  that depends on the shapes alone, rounded once.
+ * The workspace must hold kmeans_norm_grad_workspace_bytes() bytes, 256-byte
+ * aligned (0 from the query: invalid shapes), where grad_weight is given. */
+KM_API size_t kmeans_norm_grad_workspace_bytes(int64_t T, int64_t d, km_dtype xt);
+KM_API km_status kmeans_norm_grad(const void *grad, const void *h, km_dtype xt, int64_t T, int64_t d,
+                           const void *grad_residual, const void *weight, km_dtype wt, float eps, void *grad_x,
+                           void *grad_weight, void *workspace, size_t workspace_bytes, km_stream stream);
+
+/* Tokens choose experts: the gate of a layer of experts.  With p[t] the
+ * softmax of logits[t] (float32):
+ *   experts[t][k]  the token's experts of largest logit, in descending order,
+ *                  the lowest index first among equal logits; an expert whose
+ *                  logit is -infinity or NaN is never chosen, and -1 stands
+ *                  where none is left (kmeans_dispatch drops it).
+ *   weights[t][k]  normalize: the softmax over the chosen experts; else
+ *                  p[t][experts[t][k]]; 0 for -1.
+ *   counts[e]      choices of expert e; counts[E]: rows n that are not all
+ *                  -infinity.
+ *   shares[e]      sum_t p[t][e] / n (rows of -infinity have p = 0).
+ *   loss           E * sum_e shares[e] * counts[e] / sum(counts); 0 without a
+ *                  row: the loss that balances the experts.
+ *   logits   [T,E] of dtype xt; a row that is all -infinity (padding) chooses
+ *            none and counts nowhere.
+ *   experts  out [T,top] int32; weights out [T,top] float32.
+ *   counts   out [E+1] int32; shares out [E] float32; loss out [1] float32.
+ * 1 <= E <= 4096, 1 <= top <= min(E, 64), T * top < 2^31.  The
+ * workspace must hold kmeans_gate_workspace_bytes(T, E) bytes, 256-byte
+ * aligned (0 from the query: invalid shapes). */
+KM_API size_t kmeans_gate_workspace_bytes(int64_t T, int64_t E);
+KM_API km_status kmeans_gate(const void *logits, km_dtype xt, int64_t T, int64_t E, int64_t top, int32_t normalize,
+                      int32_t *experts, float *weights, int32_t *counts, float *shares, float *loss, void *workspace,
+                      size_t workspace_bytes, km_stream stream);
+
+/* Gradient of kmeans_gate's logits, for the choices made (counts are constants):
+ *   f[e]           = grad_loss * E * counts[e] / (n * sum(counts))
+ *   grad_logits[t] = p (f - <p, f>) + the chosen experts' part: with normalize
+ *                    w (gw - <w, gw>) over the chosen, else p (g - <p, g>)
+ *                    with g = gw at the chosen experts, 0 elsewhere
+ * in float32, rounded once; a row of -infinity has zeros.
+ *   experts, counts  of kmeans_gate (an expert outside [0, E) is no choice; a
+ *                    row's experts are distinct).
+ *   grad_weights     [T,top] float32 or NULL; grad_loss [1] float32 or NULL.
+ *   grad_logits      out [T,E] of dtype xt. */
+KM_API km_status kmeans_gate_grad(const void *logits, km_dtype xt, int64_t T, int64_t E, int64_t top, int32_t normalize,
+                           const int32_t *experts, const int32_t *counts, const float *grad_weights,
+                           const float *grad_loss, void *grad_logits, km_stream stream);
+
+/* The plan of kmeans_dispatch alone (the same offsets, slots and order),
+ * without copying rows: for products that gather them (kmeans_block_product's
+ * order).  The workspace must hold kmeans_plan_workspace_bytes(T, top, E)
+ * bytes, 256-byte aligned (0 from the query: none is needed, or the shapes are
+ * invalid). */
+KM_API size_t kmeans_plan_workspace_bytes(int64_t T, int64_t top, int64_t E);
+KM_API km_status kmeans_plan(const int32_t *experts, int64_t T, int64_t top, int64_t E, int32_t *offsets, int32_t *slots,
+                      int32_t *order, void *workspace, size_t workspace_bytes, km_stream stream);
+
+/* Products of 8-bit rows with 8-bit matrices, one matrix per expert.  With the
+ * values X = x * x_scales and W[e] = codes[e] * scales[e], row p of the segment
+ * offsets[e] <= p < offsets[e+1] is multiplied by its expert's matrix:
+ *   kmeans_block_product       out[p][m] = sum_k X[p][k] W[e][m][k]
+ *   kmeans_block_product_grad  out[p][k] = sum_m X[p][m] W[e][m][k]
+ * (the second is the gradient of the first's rows).  Rows past offsets[E]
+ * become zeros.  The codes' products are summed over a block of 128 by the
+ * matrix instruction, multiplied by the product of the two scales and added to
+ * float32 sums over the blocks, rounded once at the end.  The instruction aligns
+ * eight products to the largest of them and drops what lies below 2^-13 of its
+ * power of two, then adds in float32: without bias, 1.4e-5 of the result's norm
+ * for normally distributed values (their rounding to codes is 0.037 of it).
+ * Whole numbers up to 15 are summed exactly.
+ *   x         [S,K] (grad: [S,M]) codes; x_scales [S,ceil(K/128)] (grad:
+ *             [S,ceil(M/128)]) float32.
+ *   codes     [E,M,K]; scales [E,ceil(M/128),ceil(K/128)] float32.
+ *   offsets   [E+1] int32, ascending from 0, offsets[E] <= S; NULL with E == 1
+ *             means all S rows.
+ *   order, top  (product only) NULL, or the order [S] of kmeans_plan with
+ *             S = T * top choices: x and x_scales then have T rows, and row p
+ *             is row order[p] / top of them (order outside [0, S): a row of
+ *             zeros).
+ *   out       [S,M] (grad: [S,K]) of dtype ot.
+ * S, M, K <= 2^20, E <= 4096.  The workspace must hold
+ * kmeans_block_product_workspace_bytes(S, E, M, K) (grad:
+ * kmeans_block_product_grad_workspace_bytes) bytes, 256-byte aligned (0 from
+ * the query: none is needed, or the shapes are invalid). */
+KM_API size_t kmeans_block_product_workspace_bytes(int64_t S, int64_t E, int64_t M, int64_t K);
+KM_API km_status kmeans_block_product(const void *x, const float *x_scales, int64_t S, const void *codes,
+                               const float *scales, int64_t E, int64_t M, int64_t K, const int32_t *offsets,
+                               const int32_t *order, int64_t top, void *out, km_dtype ot, void *workspace,
+                               size_t workspace_bytes, km_stream stream);
+KM_API size_t kmeans_block_product_grad_workspace_bytes(int64_t S, int64_t E, int64_t M, int64_t K);
+KM_API km_status kmeans_block_product_grad(const void *grad, const float *grad_scales, int64_t S, const void *codes,
+                                    const float *scales, int64_t E, int64_t M, int64_t K, const int32_t *offsets,
+                                    void *out, km_dtype ot, void *workspace, size_t workspace_bytes, km_stream stream);
+
 /* Static description of a status code. */
 KM_API const char *kmeans_status_str(km_status status);
 
