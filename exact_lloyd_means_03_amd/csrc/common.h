@@ -97,6 +97,14 @@ __device__ __forceinline__ void dma2(const char* sbase, uint32_t voff, const voi
                  : "memory");
 }
 
+// The same from an address of every lane's own (vector registers, which need no
+// wait states): a write of M0 wants one.
+__device__ __forceinline__ void dma16_lane(const void* from, const void* lds) {
+    const uint32_t l = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) void*)lds;
+    asm volatile("s_nop 1\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(from), "{m0}"(__builtin_amdgcn_readfirstlane(l))
+                 : "memory");
+}
+
 // Lanes of the wave whose v equals this lane's (among the lanes where
 // `active` holds): one ballot per bit of the values (0 <= v < 2^nbits).
 __device__ __forceinline__ uint64_t lanes_matching(int32_t v, int nbits, bool active) {

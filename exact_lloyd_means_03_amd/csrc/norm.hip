@@ -101,7 +101,7 @@ __global__ __launch_bounds__(WPR == 1 ? 256 : 64 * WPR) void k_norm(
         if constexpr (OUT8) {
             const float s = block_scale(lane_max<LB>(top));
             uint32_t q[N / 4];
-            to_codes<N>(a[i], 1.f / s, q);
+            to_codes<N>(a[i], s, q);
             if (c < C) {
                 store_codes<N>(codes + t * d + e0, d, skip, q);
                 if (c % LB == 0) scales[t * nb + c / LB] = s;
@@ -333,7 +333,7 @@ __global__ __launch_bounds__(256) void k_quantize_rows(const T* __restrict__ x, 
     }
     const float s = block_scale(lane_max<LB>(top));
     uint32_t q[N / 4];
-    to_codes<N>(a, 1.f / s, q);
+    to_codes<N>(a, s, q);
     if (!in) return;
     store_codes<N>(codes + t * d + e0, d, skip, q);
     if (c % LB == 0) scales[t * nb + c / LB] = s;
@@ -370,14 +370,14 @@ __global__ __launch_bounds__(256) void k_quantize_matrix(const T* __restrict__ x
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < 4; ++i) top = top > s_top[i] ? top : s_top[i];
-    const float s = block_scale(top), inv = 1.f / s;
+    const float s = block_scale(top);
     if (threadIdx.x == 0) scales[at] = s;
 #pragma unroll
     for (int i = 0; i < R; ++i) {
         const int m = threadIdx.x / LB + i * STEP;
         if (m0 + m >= M || c >= C) continue;
         uint32_t q[N / 4];
-        to_codes<N>(a[i], inv, q);
+        to_codes<N>(a[i], s, q);
         store_codes<N>(codes + (int64_t)m * d + e0, d, skip, q);
     }
 }
