@@ -10,7 +10,8 @@
 
 namespace km {
 
-constexpr int kGateThreads = 256, kGateTopMax = 64;
+constexpr int kGateTopMax = 64;
+constexpr int gate_threads(int L) { return L == 16 ? 512 : 256; }  // blocks of 32 rows, or of 4
 bool gate_top_fits(int64_t top) { return top <= kGateTopMax; }
 
 // A logit as a number that orders like it: 0 for those that are never chosen
@@ -27,20 +28,30 @@ __device__ __forceinline__ float load_logit(const float* p) { return *p; }
 __device__ __forceinline__ float load_logit(const _Float16* p) { return (float)*p; }
 __device__ __forceinline__ float load_logit(const uint16_t* p) { return bf16_to_f32(*p); }
 
+// exp(x) for x <= 0 (NaN stays): 2^(x log2 e) with the product's own rounding added
+// back, 2 units in the last place in half the instructions of expf; 0 below 2^-126.
+__device__ __forceinline__ float gate_exp(float x) {
+    x = x < -150.f ? -150.f : x;
+    const float t = x * 1.44269502f, rest = fmaf(x, 1.92596299e-8f, fmaf(x, 1.44269502f, -t));
+    const float r = __builtin_amdgcn_exp2f(t);
+    return fmaf(r, rest * 0.693147182f, r);
+}
+
 // z[j] = exp(l[j] - m), m the largest logit that is a number; returns 1 / sum z
 // (0 for a row of -infinity; NaN where a logit is NaN or +infinity).
 template <int L, int EPL>
-__device__ __forceinline__ float gate_softmax(const float (&l)[EPL], const uint32_t (&key)[EPL], float (&z)[EPL],
-                                              float* m_out) {
-    uint32_t top = 0;
+__device__ __forceinline__ float gate_softmax(const float (&l)[EPL], float (&z)[EPL], float* m_out) {
+    float m = -INFINITY;
 #pragma unroll
-    for (int j = 0; j < EPL; ++j) top = top > key[j] ? top : key[j];
-    top = lane_max<L>(top);
-    const float m = top ? gate_value(top) : 0.f;
+    for (int j = 0; j < EPL; ++j) m = fmaxf(m, l[j]);  // (NaN is passed over)
+    m = __uint_as_float(lane_fold<L>(__float_as_uint(m), [](uint32_t a, uint32_t b) {
+        return __float_as_uint(fmaxf(__uint_as_float(a), __uint_as_float(b)));
+    }));
+    m = m > -INFINITY ? m : 0.f;
     float sum = 0.f;
 #pragma unroll
     for (int j = 0; j < EPL; ++j) {
-        z[j] = expf(l[j] - m);
+        z[j] = gate_exp(l[j] - m);
         sum += z[j];
     }
     sum = lane_sum<L>(sum);
@@ -48,17 +59,31 @@ __device__ __forceinline__ float gate_softmax(const float (&l)[EPL], const uint3
     return sum == 0.f ? 0.f : 1.f / sum;
 }
 
+// E sum_e shares[e] counts[e] / sum(counts) from dot = sum_e shares[e] counts[e]
+// (NaN shares make a NaN loss, also where no expert could be chosen).
+__device__ __forceinline__ float gate_loss(float dot, int64_t choices, int E) {
+    return choices ? dot * ((float)E / (float)choices) : dot * 0.f;
+}
+
+struct GateSum {
+    float dot;
+    int32_t all;
+};
+
 // Blocks of the gate leave their counts and probabilities' sums: part_n[b][E + 1]
-// (the last one: rows that are not all -infinity) and part_p[b][E].
-template <typename T, int L, int EPL>
-__global__ __launch_bounds__(kGateThreads) void k_gate(const T* __restrict__ logits, int64_t Tn, int E, int top,
+// (the last one: rows that are not all -infinity) and part_p[b][E].  A single
+// block has them all and finishes by itself.
+template <typename T, int L, int EPL, int KR>
+__global__ __launch_bounds__(gate_threads(L)) void k_gate(const T* __restrict__ logits, int64_t Tn, int E, int top,
                                                        bool normalize, int32_t* __restrict__ experts,
                                                        float* __restrict__ weights, int32_t* __restrict__ part_n,
-                                                       float* __restrict__ part_p) {
-    constexpr int G = kGateThreads / L, KR = kGateTopMax / L, GW = 64 / L;
-    extern __shared__ int32_t s_cnt[];  // [E + 1]; then float [4][E]
+                                                       float* __restrict__ part_p, int32_t* __restrict__ ticket,
+                                                       int32_t* __restrict__ counts, float* __restrict__ shares,
+                                                       float* __restrict__ loss) {
+    constexpr int NT = gate_threads(L), G = NT / L, GW = 64 / L, W = NT / 64;
+    extern __shared__ int32_t s_cnt[];  // [E + 1]; then float [W][E]
     const int tid = threadIdx.x, lane = tid & (L - 1), grp = tid / L;
-    for (int j = tid; j <= E; j += kGateThreads) s_cnt[j] = 0;
+    for (int j = tid; j <= E; j += NT) s_cnt[j] = 0;
     __syncthreads();
     float acc[EPL];
 #pragma unroll
@@ -76,39 +101,50 @@ __global__ __launch_bounds__(kGateThreads) void k_gate(const T* __restrict__ log
             l[j] = in && e < E ? load_logit(logits + t * E + e) : -INFINITY;
             key[j] = gate_key(l[j]);
         }
-        const float inv = gate_softmax<L, EPL>(l, key, z, &m);
+        const float inv = gate_softmax<L, EPL>(l, z, &m);
         if (inv != 0.f) {
             rows += lane == 0;
 #pragma unroll
             for (int j = 0; j < EPL; ++j) acc[j] = fmaf(z[j], inv, acc[j]);
         }
-        float zk[KR], sum = 0.f;  // the choice k of lane k % L (-1: none)
+        uint32_t kk[KR], ke[KR];  // the choice k is lane k % L's: its key (0: none) and expert
 #pragma unroll
-        for (int u = 0; u < KR; ++u) zk[u] = -1.f;
+        for (int u = 0; u < KR; ++u) kk[u] = 0, ke[u] = ~0u;
         for (int k = 0; k < top; ++k) {
-            uint32_t best = 0, at = 0;
+            uint32_t most = 0, at = 0;
 #pragma unroll
-            for (int j = 0; j < EPL; ++j) {
-                if (key[j] > best) best = key[j], at = j;
+            for (int j = 0; j < EPL; ++j) most = most > key[j] ? most : key[j];
+            most = lane_max<L>(most);
+#pragma unroll
+            for (int j = EPL - 1; j >= 0; --j) at = key[j] == most ? (uint32_t)(j * L + lane) + 1 : at;
+            const uint32_t e = lane_min<L>(at - 1);  // (a lane without it: the largest number)
+            if (most && e % L == (uint32_t)lane) atomicAdd(&s_cnt[e], 1);
+            uint32_t gone = most && e % L == (uint32_t)lane ? e / L : ~0u;
+            asm("" : "+v"(gone));  // (one comparison for each register below)
+#pragma unroll
+            for (int j = 0; j < EPL; ++j) key[j] = gone == (uint32_t)j ? 0u : key[j];
+#pragma unroll
+            for (int u = 0; u < KR; ++u) {
+                const bool here = k == u * L + lane;
+                kk[u] = here ? most : kk[u];
+                ke[u] = here && most ? e : ke[u];
             }
-            const uint32_t most = lane_max<L>(best);
-            const uint32_t e = lane_min<L>(best == most && most ? at * L + lane : 0xffffffffu);
-            if (e % L == (uint32_t)lane && most) {
-#pragma unroll
-                for (int j = 0; j < EPL; ++j) key[j] = e / L == (uint32_t)j ? 0u : key[j];
-                atomicAdd(&s_cnt[e], 1);
-            }
-            const float v = most ? expf(gate_value(most) - m) : -1.f;
-            sum += most ? v : 0.f;
-#pragma unroll
-            for (int u = 0; u < KR; ++u) zk[u] = k == u * L + lane ? v : zk[u];
-            if (in && lane == 0) experts[t * top + k] = most ? (int32_t)e : -1;
         }
+        float zk[KR], sum = 0.f;
+#pragma unroll
+        for (int u = 0; u < KR; ++u) {
+            zk[u] = kk[u] ? gate_exp(gate_value(kk[u]) - m) : 0.f;
+            sum += zk[u];
+        }
+        sum = lane_sum<L>(sum);
         const float by = !normalize ? inv : sum == 0.f ? 0.f : 1.f / sum;
 #pragma unroll
         for (int u = 0; u < KR; ++u) {
             const int k = u * L + lane;
-            if (in && k < top) weights[t * top + k] = zk[u] < 0.f ? 0.f : zk[u] * by;
+            if (in && k < top) {
+                experts[t * top + k] = (int32_t)ke[u];
+                weights[t * top + k] = kk[u] ? zk[u] * by : 0.f;
+            }
         }
     }
     // the groups of a wave, then the waves, in order
@@ -124,60 +160,152 @@ __global__ __launch_bounds__(kGateThreads) void k_gate(const T* __restrict__ log
     }
     if (rows) atomicAdd(&s_cnt[E], rows);
     __syncthreads();
+    if (gridDim.x == 1) {
+        const int32_t n = s_cnt[E];
+        const float inv = n ? 1.f / (float)n : 0.f;
+        float dot = 0.f;
+        int32_t all = 0;
+        for (int e = tid; e < E; e += NT) {
+            float p = s_p[e];
+            for (int i = 1; i < W; ++i) p += s_p[i * E + e];
+            p *= inv;
+            counts[e] = s_cnt[e];
+            shares[e] = p;
+            all += s_cnt[e];
+            dot = fmaf((float)s_cnt[e], p, dot);
+        }
+        if (tid == 0) counts[E] = n;
+        dot = lane_sum<64>(dot);
+        all = (int32_t)lane_fold<64>((uint32_t)all, [](uint32_t a, uint32_t b) { return a + b; });
+        __shared__ GateSum s_sum[W];
+        if ((tid & 63) == 0) s_sum[tid >> 6] = {dot, all};
+        __syncthreads();
+        if (tid == 0) {
+            int64_t c = 0;
+            dot = 0.f;
+            for (int i = 0; i < W; ++i) dot += s_sum[i].dot, c += s_sum[i].all;
+            loss[0] = gate_loss(dot, c, E);
+        }
+        return;
+    }
+    if (blockIdx.x == 0 && tid == 0) *ticket = 0;
     int32_t* pn = part_n + (int64_t)blockIdx.x * (E + 1);
     float* pp = part_p + (int64_t)blockIdx.x * E;
-    for (int e = tid; e <= E; e += kGateThreads) {
+    for (int e = tid; e <= E; e += NT) {
         pn[e] = s_cnt[e];
-        if (e < E) pp[e] = ((s_p[e] + s_p[E + e]) + s_p[2 * E + e]) + s_p[3 * E + e];
-    }
-}
-
-// Counts and shares of the blocks' parts, and the loss: one block.
-__global__ __launch_bounds__(1024) void k_gate_fold(const int32_t* __restrict__ part_n, const float* __restrict__ part_p,
-                                                    int nblk, int E, int32_t* __restrict__ counts,
-                                                    float* __restrict__ shares, float* __restrict__ loss) {
-    __shared__ float s_f[1024];
-    __shared__ int64_t s_n[1024];
-    const int tid = threadIdx.x;
-    int32_t n = 0;
-    for (int b = 0; b < nblk; ++b) n += part_n[(int64_t)b * (E + 1) + E];
-    const float inv = n ? 1.f / (float)n : 0.f;
-    float dot = 0.f;
-    int64_t all = 0;
-    for (int e = tid; e < E; e += 1024) {
-        int32_t c = 0;
-        float p = 0.f;
-        for (int b = 0; b < nblk; ++b) {
-            c += part_n[(int64_t)b * (E + 1) + e];
-            p += part_p[(int64_t)b * E + e];
+        if (e < E) {
+            float p = s_p[e];
+            for (int i = 1; i < W; ++i) p += s_p[i * E + e];
+            pp[e] = p;
         }
-        p *= inv;
-        counts[e] = c;
-        shares[e] = p;
-        all += c;
-        dot = fmaf((float)c, p, dot);
-    }
-    s_f[tid] = dot;
-    s_n[tid] = all;
-    __syncthreads();
-    for (int o = 512; o >= 1; o >>= 1) {
-        if (tid < o) s_f[tid] += s_f[tid + o], s_n[tid] += s_n[tid + o];
-        __syncthreads();
-    }
-    if (tid == 0) {
-        counts[E] = n;
-        // (NaN shares make a NaN loss, also where no expert could be chosen)
-        loss[0] = s_n[0] ? s_f[0] * (float)E / (float)s_n[0] : s_f[0] * 0.f;
     }
 }
 
+// Counts and shares of the blocks' parts, 16 experts a block: 64 groups of 16
+// threads take every 64th part, then their sums in order.  The block that comes
+// last adds all blocks' parts of the loss, in order.
+constexpr int kFoldExperts = 16, kFoldParts = 64;
+
+__global__ __launch_bounds__(kFoldExperts* kFoldParts) void k_gate_fold(
+    const int32_t* __restrict__ part_n, const float* __restrict__ part_p, int nblk, int E, GateSum* __restrict__ sums,
+    int32_t* __restrict__ ticket, int32_t* __restrict__ counts, float* __restrict__ shares, float* __restrict__ loss) {
+    constexpr int W = kFoldExperts * kFoldParts / 64;
+    __shared__ float s_p[W][kFoldExperts];
+    __shared__ int32_t s_c[W][kFoldExperts], s_n[W];
+    const int tid = threadIdx.x, j = tid % kFoldExperts, h = tid / kFoldExperts;
+    const int e = blockIdx.x * kFoldExperts + j;
+    float p = 0.f;
+    int32_t c = 0, n = 0;
+    const int at = e < E ? e : E - 1;
+    constexpr int U = 8;  // parts in flight: their loads are what a block waits for
+    for (int b0 = h; b0 < nblk; b0 += U * kFoldParts) {
+        float pv[U];
+        int32_t cv[U], nv[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int b = b0 + u * kFoldParts < nblk ? b0 + u * kFoldParts : b0;
+            pv[u] = part_p[(int64_t)b * E + at];
+            cv[u] = part_n[(int64_t)b * (E + 1) + at];
+            nv[u] = part_n[(int64_t)b * (E + 1) + E];
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (b0 + u * kFoldParts < nblk) p += pv[u], c += cv[u], n += j == 0 ? nv[u] : 0;
+        }
+    }
+    auto over = [&]() {  // the four parts of a wave
+        p += __shfl_xor(p, 16, 64);
+        c += __shfl_xor(c, 16, 64);
+        n += __shfl_xor(n, 16, 64);
+        p += __shfl_xor(p, 32, 64);
+        c += __shfl_xor(c, 32, 64);
+        n += __shfl_xor(n, 32, 64);
+    };
+    over();
+    if ((tid & 63) < kFoldExperts) s_p[tid >> 6][j] = p, s_c[tid >> 6][j] = c;
+    if ((tid & 63) == 0) s_n[tid >> 6] = n;
+    __syncthreads();
+    if (tid < 64) {  // the first wave: lane j an expert, four quarters of the waves
+        p = 0.f;
+        c = n = 0;
+#pragma unroll
+        for (int i = 0; i < W / 4; ++i) p += s_p[h * (W / 4) + i][j], c += s_c[h * (W / 4) + i][j], n += s_n[h * (W / 4) + i];
+        over();
+        if (tid < kFoldExperts && e < E) {
+            p *= n ? 1.f / (float)n : 0.f;
+            counts[e] = c;
+            shares[e] = p;
+        } else {
+            p = 0.f;
+            c = 0;
+        }
+        const float dot = lane_sum<64>((float)c * p);
+        c = (int32_t)lane_fold<64>((uint32_t)c, [](uint32_t a, uint32_t b) { return a + b; });
+        if (tid == 0) {
+            if (blockIdx.x == 0) counts[E] = n;
+            __hip_atomic_store(&sums[blockIdx.x].dot, dot, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            __hip_atomic_store(&sums[blockIdx.x].all, c, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            if (__hip_atomic_fetch_add(ticket, 1, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT) == (int)gridDim.x - 1) {
+                float d = 0.f;
+                int64_t a = 0;
+                for (int i = 0; i < (int)gridDim.x; ++i) {
+                    d += __hip_atomic_load(&sums[i].dot, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+                    a += __hip_atomic_load(&sums[i].all, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+                }
+                loss[0] = gate_loss(d, a, E);
+            }
+        }
+    }
+}
+
+static int64_t gate_rows(int64_t E) { return E <= 256 ? gate_threads(16) / 16 : gate_threads(64) / 64; }
+
+// Blocks of the gate: one where few rows make at most two rounds of it (a second
+// launch costs more), else one for every round of rows, as far as their parts are
+// no more than 4 MB or 256 rows of them.
 static int64_t gate_blocks(int64_t T, int64_t E) {
-    const int64_t rows = E <= 256 ? kGateThreads / 16 : kGateThreads / 64, n = (T + rows - 1) / rows;
-    return n < 1 ? 1 : n < 256 ? n : 256;
+    const int64_t rows = gate_rows(E), n = (T + rows - 1) / rows;
+    if (n <= 2) return 1;
+    int64_t most = ((int64_t)1 << 19) / E;
+    most = most < 256 ? 256 : most > 2048 ? 2048 : most;
+    const int64_t rounds = (n + most - 1) / most;
+    return (n + rounds - 1) / rounds;
 }
-size_t gate_scratch(int64_t T, int64_t E) {
-    return ((size_t)gate_blocks(T, E) * (2 * E + 1) * sizeof(int32_t) + 255) & ~(size_t)255;
+struct GatePlan {
+    size_t part_n = 0, part_p = 0, sums = 0, ticket = 0, total = 0;
+};
+static GatePlan plan_gate(int64_t T, int64_t E) {
+    GatePlan p;
+    const int64_t nblk = gate_blocks(T, E);
+    if (nblk == 1) return p;
+    auto up = [](size_t v) { return (v + 255) & ~(size_t)255; };
+    p.part_p = up((size_t)nblk * (E + 1) * sizeof(int32_t));
+    p.sums = p.part_p + up((size_t)nblk * E * sizeof(float));
+    p.ticket = p.sums + up((size_t)((E + kFoldExperts - 1) / kFoldExperts) * sizeof(GateSum));
+    p.total = p.ticket + 256;
+    return p;
 }
+size_t gate_scratch(int64_t T, int64_t E) { return plan_gate(T, E).total; }
 
 #define KM_GATE(T)                          \
     do {                                    \
@@ -195,24 +323,35 @@ size_t gate_scratch(int64_t T, int64_t E) {
 hipError_t launch_gate(DType xt, const void* logits, int64_t T, int64_t E, int64_t top, bool normalize, int32_t* experts,
                        float* weights, int32_t* counts, float* shares, float* loss, void* ws, hipStream_t s) {
     const int64_t nblk = gate_blocks(T, E);
-    int32_t* pn = (int32_t*)ws;
-    float* pp = (float*)(pn + nblk * (E + 1));
-    const size_t lds = (size_t)(5 * E + 1) * sizeof(int32_t);
+    const GatePlan p = plan_gate(T, E);
+    int32_t* pn = (int32_t*)((char*)ws + p.part_n);
+    float* pp = (float*)((char*)ws + p.part_p);
+    int32_t* ticket = (int32_t*)((char*)ws + p.ticket);
+    const size_t lds = (size_t)(E + 1 + (E <= 256 ? gate_threads(16) : gate_threads(64)) / 64 * E) * sizeof(int32_t);
     hipError_t e = hipSuccess;
-#define KM_GO(TT, L, EPL)                                                                                             \
-    do {                                                                                                              \
-        if (lds > 64 * 1024 && (e = hipFuncSetAttribute((const void*)k_gate<TT, L, EPL>,                              \
+#define KM_GO2(TT, L, EPL, KR)                                                                                         \
+    do {                                                                                                               \
+        if (lds > 64 * 1024 && (e = hipFuncSetAttribute((const void*)k_gate<TT, L, EPL, KR>,                           \
                                                         hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds)) != hipSuccess) \
-            return e;                                                                                                 \
-        hipLaunchKernelGGL((k_gate<TT, L, EPL>), dim3((unsigned)nblk), dim3(kGateThreads), lds, s, (const TT*)logits, \
-                           T, (int)E, (int)top, normalize, experts, weights, pn, pp);                                 \
+            return e;                                                                                                  \
+        hipLaunchKernelGGL((k_gate<TT, L, EPL, KR>), dim3((unsigned)nblk), dim3(gate_threads(L)), lds, s,              \
+                           (const TT*)logits, T, (int)E, (int)top, normalize, experts, weights, pn, pp, ticket,        \
+                           counts, shares, loss);                                                                      \
+    } while (0)
+#define KM_GO(TT, L, EPL)                               \
+    do {                                                \
+        if (top <= L) KM_GO2(TT, L, EPL, 1);            \
+        else KM_GO2(TT, L, EPL, kGateTopMax / L);       \
     } while (0)
     if (xt == DType::F32) KM_GATE(float);
     else if (xt == DType::F16) KM_GATE(_Float16);
     else KM_GATE(uint16_t);
 #undef KM_GO
-    if ((e = hipGetLastError()) != hipSuccess) return e;
-    hipLaunchKernelGGL(k_gate_fold, dim3(1), dim3(1024), 0, s, pn, pp, (int)nblk, (int)E, counts, shares, loss);
+#undef KM_GO2
+    if ((e = hipGetLastError()) != hipSuccess || nblk == 1) return e;
+    hipLaunchKernelGGL(k_gate_fold, dim3((unsigned)((E + kFoldExperts - 1) / kFoldExperts)),
+                       dim3(kFoldExperts * kFoldParts), 0, s, pn, pp, (int)nblk, (int)E, (GateSum*)((char*)ws + p.sums),
+                       ticket, counts, shares, loss);
     return hipGetLastError();
 }
 
@@ -220,12 +359,12 @@ hipError_t launch_gate(DType xt, const void* logits, int64_t T, int64_t E, int64
 // through LDS: a group writes its row, the lanes of the choices add to it, the
 // group reads it back.
 template <typename T, int L, int EPL>
-__global__ __launch_bounds__(kGateThreads) void k_gate_grad(const T* __restrict__ logits, int64_t Tn, int E, int top,
+__global__ __launch_bounds__(gate_threads(L)) void k_gate_grad(const T* __restrict__ logits, int64_t Tn, int E, int top,
                                                             bool normalize, const int32_t* __restrict__ experts,
                                                             const int32_t* __restrict__ counts,
                                                             const float* __restrict__ gweights,
                                                             const float* __restrict__ gloss, T* __restrict__ out) {
-    constexpr int G = kGateThreads / L, KR = kGateTopMax / L;
+    constexpr int G = gate_threads(L) / L, KR = kGateTopMax / L;
     extern __shared__ float s_row[];  // [G][EPL L]
     const int lane = threadIdx.x & (L - 1), grp = threadIdx.x / L;
     float* row = s_row + grp * EPL * L;
@@ -249,12 +388,10 @@ __global__ __launch_bounds__(kGateThreads) void k_gate_grad(const T* __restrict_
         const int64_t t = t0 + grp;
         const bool in = t < Tn;
         float l[EPL], z[EPL], m;
-        uint32_t key[EPL];
 #pragma unroll
         for (int j = 0; j < EPL; ++j) {
             const int e = j * L + lane;
             l[j] = in && e < E ? load_logit(logits + t * E + e) : -INFINITY;
-            key[j] = gate_key(l[j]);
         }
         int32_t ek[KR];
         float gk[KR], lk[KR];
@@ -267,12 +404,12 @@ __global__ __launch_bounds__(kGateThreads) void k_gate_grad(const T* __restrict_
             if ((uint32_t)ek[u] >= (uint32_t)E) ek[u] = -1;
             lk[u] = ek[u] >= 0 ? load_logit(logits + t * E + ek[u]) : -INFINITY;
         }
-        const float inv = gate_softmax<L, EPL>(l, key, z, &m);
+        const float inv = gate_softmax<L, EPL>(l, z, &m);
         // the choices' softmax numerators, and <w, gw> over the chosen
         float wk[KR], sum = 0.f, dot = 0.f;
 #pragma unroll
         for (int u = 0; u < KR; ++u) {
-            wk[u] = ek[u] >= 0 ? expf(lk[u] - m) : 0.f;
+            wk[u] = ek[u] >= 0 ? gate_exp(lk[u] - m) : 0.f;
             sum += wk[u];
             if (ek[u] >= 0) dot = fmaf(wk[u], gk[u], dot);
         }
@@ -306,13 +443,13 @@ hipError_t launch_gate_grad(DType xt, const void* logits, int64_t T, int64_t E, 
                             const int32_t* experts, const int32_t* counts, const float* gweights, const float* gloss,
                             void* out, hipStream_t s) {
     if (T == 0) return hipSuccess;
-    const int64_t rows = E <= 256 ? kGateThreads / 16 : kGateThreads / 64, n = (T + rows - 1) / rows;
+    const int64_t rows = gate_rows(E), n = (T + rows - 1) / rows;
     const unsigned nblk = (unsigned)(n < 2048 ? n : 2048);
     hipError_t e = hipSuccess;
 #define KM_GO(TT, L, EPL)                                                                                              \
     do {                                                                                                               \
-        constexpr size_t lds = (size_t)kGateThreads * EPL * sizeof(float);                                             \
-        hipLaunchKernelGGL((k_gate_grad<TT, L, EPL>), dim3(nblk), dim3(kGateThreads), lds, s, (const TT*)logits, T,    \
+        constexpr size_t lds = (size_t)gate_threads(L) * EPL * sizeof(float);                                             \
+        hipLaunchKernelGGL((k_gate_grad<TT, L, EPL>), dim3(nblk), dim3(gate_threads(L)), lds, s, (const TT*)logits, T,    \
                            (int)E, (int)top, normalize, experts, counts, gweights, gloss, (TT*)out);                   \
     } while (0)
     if (xt == DType::F32) KM_GATE(float);

@@ -11,7 +11,7 @@ from __future__ import annotations
 import torch
 
 from . import _lib
-from .api import _DT, _bytes, _no_buffers, _no_gradient, _output, _ptr, _stream, _tensor, kmeans_combine
+from .api import _DT, _bytes, _no_buffers, _no_gradient, _ptr, _stream, _tensor, kmeans_combine
 
 E4M3 = torch.float8_e4m3fn
 BLOCK = 128
@@ -23,13 +23,30 @@ def _blocks(n):
 
 def _grads(*tensors):
     """Whether autograd records a call of these inputs (None among them)."""
-    return torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors)
+    for t in tensors:
+        if t is not None and t.requires_grad:
+            return torch.is_grad_enabled()
+    return False
+
+
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
+
+def _output(t, name, dev, dtype, shape):
+    """The caller's output, or a new one (the least of torch's ways to make one)."""
+    if t is not None:
+        return _tensor(t, name, dev, dtype, shape)
+    strides, n = (), 1
+    for size in reversed(shape):
+        strides = (n, *strides)
+        n *= size
+    return torch.empty_strided(shape, strides, dtype=dtype, device=dev)
 
 
 def _call(name, dev, *args):
     """The entry point on the current stream of dev, with dev current (kernels are launched on the current device)."""
-    fn = getattr(_lib.load(), name)
-    if dev.index is None or dev.index == torch.cuda.current_device():
+    fn = getattr(_lib._lib or _lib.load(), name)
+    if dev.index is None or dev.index == _current_device():
         st = fn(*args, _stream(dev))
     else:
         with torch.cuda.device(dev):
@@ -38,8 +55,15 @@ def _call(name, dev, *args):
         _lib.check(st, name)
 
 
-def _codes(t, name, dev, shape):
-    return torch.empty(shape, dtype=E4M3, device=dev) if t is None else _tensor(t, name, dev, E4M3, shape)
+def _workspace(ws, n, dev):
+    """The caller's workspace, or one of n bytes (None: none is needed)."""
+    if ws is not None:
+        return _tensor(ws, "workspace", dev, torch.uint8, None)
+    return torch.empty(n, dtype=torch.uint8, device=dev) if n else None
+
+
+def _ws_args(ws):
+    return (None, 0) if ws is None else (ws.data_ptr(), ws.numel())
 
 
 # 8-bit codes ---------------------------------------------------------------
@@ -58,7 +82,7 @@ def kmeans_quantize(x, rows: int = 1, codes=None, scales=None):
         _no_gradient("kmeans_quantize", x=x)
     dev, shape = x.device, tuple(x.shape)
     M, K = shape[-2:]
-    codes = _codes(codes, "codes", dev, shape)
+    codes = _output(codes, "codes", dev, E4M3, shape)
     scales = _output(scales, "scales", dev, torch.float32, (*shape[:-2], -(-M // rows), _blocks(K)))
     _call("kmeans_quantize", dev, x.data_ptr(), _DT[x.dtype], shape[0] if len(shape) == 3 else 1, M, K, rows,
           codes.data_ptr(), scales.data_ptr())
@@ -110,7 +134,7 @@ def kmeans_norm_quantize(x, weight=None, eps: float = 1e-6, residual=None, codes
     dev, dt, T, d = _norm_inputs(x, weight, residual, "x")
     if _grads(x, weight, residual):
         _no_gradient("kmeans_norm_quantize", x=x, weight=weight, residual=residual)
-    codes = _codes(codes, "codes", dev, (T, d))
+    codes = _output(codes, "codes", dev, E4M3, (T, d))
     scales = _output(scales, "scales", dev, torch.float32, (T, _blocks(d)))
     if residual is None:
         h = x
@@ -140,9 +164,9 @@ def kmeans_norm_grad(grad, h, weight=None, eps: float = 1e-6, grad_residual=None
         grad_weight = None
     else:
         grad_weight = _output(grad_weight, "grad_weight", dev, weight.dtype, (d,))
-        ws = norm_grad_workspace(T, d, dt, dev) if ws is None else _tensor(ws, "workspace", dev, torch.uint8, None)
+        ws = _workspace(ws, 0 if ws is not None else _lib.load().kmeans_norm_grad_workspace_bytes(T, d, _DT[dt]), dev)
     _call("kmeans_norm_grad", dev, grad.data_ptr(), h.data_ptr(), _DT[dt], T, d, _ptr(grad_residual),
-          *_weight_args(weight, dt), eps, grad_x.data_ptr(), _ptr(grad_weight), _ptr(ws), 0 if ws is None else ws.numel())
+          *_weight_args(weight, dt), eps, grad_x.data_ptr(), _ptr(grad_weight), *_ws_args(ws))
     return grad_x, grad_weight
 
 
@@ -172,14 +196,22 @@ def kmeans_gate(logits, top: int, normalize: bool = True, experts=None, weights=
     if _grads(logits):
         _no_buffers("kmeans_gate", experts, weights, counts, shares, loss)
         return _Gate.apply(logits, top, normalize, ws)
-    experts = _output(experts, "experts", dev, torch.int32, (T, top))
-    weights = _output(weights, "weights", dev, torch.float32, (T, top))
-    counts = _output(counts, "counts", dev, torch.int32, (E + 1,))
-    shares = _output(shares, "shares", dev, torch.float32, (E,))
-    loss = _output(loss, "loss", dev, torch.float32, ())
-    ws = gate_workspace(T, E, dev) if ws is None else _tensor(ws, "workspace", dev, torch.uint8, None)
+    n = T * top
+    if n and top > 0 and experts is weights is counts is shares is loss is None:
+        # five small outputs in one allocation
+        experts, weights, counts, shares, loss = torch.unsafe_split_with_sizes(
+            torch.empty_strided((2 * n + 2 * E + 2,), (1,), dtype=torch.float32, device=dev), (n, n, E + 1, E, 1))
+        experts, weights = experts.view(torch.int32).view(T, top), weights.view(T, top)
+        counts, loss = counts.view(torch.int32), loss.view(())
+    else:
+        experts = _output(experts, "experts", dev, torch.int32, (T, top))
+        weights = _output(weights, "weights", dev, torch.float32, (T, top))
+        counts = _output(counts, "counts", dev, torch.int32, (E + 1,))
+        shares = _output(shares, "shares", dev, torch.float32, (E,))
+        loss = _output(loss, "loss", dev, torch.float32, ())
+    ws = _workspace(ws, 0 if ws is not None else _lib.load().kmeans_gate_workspace_bytes(T, E), dev)
     _call("kmeans_gate", dev, logits.data_ptr(), _DT[logits.dtype], T, E, top, int(normalize), experts.data_ptr(),
-          weights.data_ptr(), counts.data_ptr(), shares.data_ptr(), loss.data_ptr(), ws.data_ptr(), ws.numel())
+          weights.data_ptr(), counts.data_ptr(), shares.data_ptr(), loss.data_ptr(), *_ws_args(ws))
     return experts, weights, counts, shares, loss
 
 
@@ -222,9 +254,9 @@ def kmeans_plan(experts, E: int, plan=None, ws=None):
     offsets = _output(offsets, "offsets", dev, torch.int32, (E + 1,))
     slots = _output(slots, "slots", dev, torch.int32, (T, top))
     order = _output(order, "order", dev, torch.int32, (T * top,))
-    ws = plan_workspace(T, top, E, dev) if ws is None else _tensor(ws, "workspace", dev, torch.uint8, None)
+    ws = _workspace(ws, 0 if ws is not None else _lib.load().kmeans_plan_workspace_bytes(T, top, E), dev)
     _call("kmeans_plan", dev, experts.data_ptr(), T, top, E, offsets.data_ptr(), slots.data_ptr(), order.data_ptr(),
-          ws.data_ptr(), ws.numel())
+          *_ws_args(ws))
     return offsets, slots, order
 
 
@@ -319,9 +351,9 @@ def kmeans_block_product(x, x_scales, codes, scales, offsets=None, order=None, d
         return _BlockProduct.apply(x, codes, scales, offsets, order, dtype)
     x, x_scales = _rows8(x, x_scales, "x", K)
     out = _output(out, "out", dev, dtype, (S, M))
-    ws = block_product_workspace(S, E, M, K, dev) if ws is None else _tensor(ws, "workspace", dev, torch.uint8, None)
+    ws = _workspace(ws, 0 if ws is not None else _lib.load().kmeans_block_product_workspace_bytes(S, E, M, K), dev)
     _call("kmeans_block_product", dev, x.data_ptr(), x_scales.data_ptr(), S, codes.data_ptr(), scales.data_ptr(), E, M, K,
-          _ptr(offsets), _ptr(order), top, out.data_ptr(), _DT[dtype], ws.data_ptr(), ws.numel())
+          _ptr(offsets), _ptr(order), top, out.data_ptr(), _DT[dtype], *_ws_args(ws))
     return out
 
 
@@ -341,10 +373,9 @@ def kmeans_block_product_grad(grad, grad_scales, codes, scales, offsets=None, dt
         _no_gradient("kmeans_block_product_grad", grad=grad, grad_scales=grad_scales, codes=codes, scales=scales)
     grad, grad_scales = _rows8(grad, grad_scales, "grad", M)
     out = _output(out, "out", dev, dtype, (S, K))
-    ws = block_product_grad_workspace(S, E, M, K, dev) if ws is None else \
-        _tensor(ws, "workspace", dev, torch.uint8, None)
+    ws = _workspace(ws, 0 if ws is not None else _lib.load().kmeans_block_product_grad_workspace_bytes(S, E, M, K), dev)
     _call("kmeans_block_product_grad", dev, grad.data_ptr(), grad_scales.data_ptr(), S, codes.data_ptr(),
-          scales.data_ptr(), E, M, K, _ptr(offsets), out.data_ptr(), _DT[dtype], ws.data_ptr(), ws.numel())
+          scales.data_ptr(), E, M, K, _ptr(offsets), out.data_ptr(), _DT[dtype], *_ws_args(ws))
     return out
 
 

@@ -494,7 +494,7 @@ KM_API km_status kmeans_norm_grad(const void *grad, const void *h, km_dtype xt, 
  *   counts   out [E+1] int32; shares out [E] float32; loss out [1] float32.
  * 1 <= E <= 4096, 1 <= top <= min(E, 64), T * top < 2^31.  The
  * workspace must hold kmeans_gate_workspace_bytes(T, E) bytes, 256-byte
- * aligned (0 from the query: invalid shapes). */
+ * aligned (0 from the query: none is needed, or the shapes are invalid). */
 KM_API size_t kmeans_gate_workspace_bytes(int64_t T, int64_t E);
 KM_API km_status kmeans_gate(const void *logits, km_dtype xt, int64_t T, int64_t E, int64_t top, int32_t normalize,
                       int32_t *experts, float *weights, int32_t *counts, float *shares, float *loss, void *workspace,

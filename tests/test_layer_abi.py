@@ -61,7 +61,7 @@ def test_norm_grad_rejects(lib):
 
 def test_gate_rejects(lib):
     q = lib.kmeans_gate_workspace_bytes
-    assert q(5000, 64) >= 64 * 8 and q(5000, 64) % 256 == 0 and q(0, 8) > 0
+    assert q(5000, 64) >= 64 * 8 and q(5000, 64) % 256 == 0 and q(24, 64) == q(0, 8) == 0
     assert q(-1, 8) == 0 and q(5, 0) == 0 and q(5, 4097) == 0
     call = _call(lib.kmeans_gate, dict(logits=FAKE, xt=F32, T=100, E=8, top=2, normalize=1, experts=FAKE, weights=FAKE,
                                        counts=FAKE, shares=FAKE, loss=FAKE, ws=WS, ws_bytes=1 << 30, stream=None))
@@ -69,7 +69,7 @@ def test_gate_rejects(lib):
         assert call(**{name: None}) == 1 and name.encode() in lib.kmeans_last_error()
     assert call(top=0) == 1 and call(top=9) == 1 and call(E=100, top=65) == 2 and call(E=0) == 1 and call(E=5000) == 2
     assert call(T=-1) == 1 and call(T=1 << 31) == 2 and call(T=1 << 30, top=2) == 2 and call(xt=8) == 2
-    assert call(ws=None) == 1 and call(ws_bytes=16) == 3
+    assert call(T=1000, ws=None) == 1 and call(T=1000, ws_bytes=16) == 3
     grad = _call(lib.kmeans_gate_grad, dict(logits=FAKE, xt=F32, T=100, E=8, top=2, normalize=1, experts=FAKE, counts=FAKE,
                                             grad_weights=FAKE, grad_loss=FAKE, grad_logits=FAKE, stream=None))
     for name in ("logits", "experts", "counts", "grad_logits"):
