@@ -18,7 +18,7 @@ __device__ __forceinline__ i32x8 join8(u32x4 a, u32x4 b) {
 
 typedef u32x4 u32x4_byte __attribute__((aligned(1)));
 
-// 16 bytes moved down by `by` (0 .. 15), zeros behind them.
+// 16 bytes moved down by `by` (0 .. 16), zeros behind them.
 __device__ __forceinline__ u32x4 move_down(u32x4 t, int by) {
     const int words = by >> 2, bits = (by & 3) * 8;
     u32x4 v;
@@ -49,6 +49,12 @@ __device__ __forceinline__ u32x4 load16_end(const uint8_t* __restrict__ p, int n
         for (int j = 0; j < 4; ++j) v[j] |= i >> 2 == j ? c : 0u;
     }
     return v;
+}
+
+// The same without branches, of a row that has 16 codes at least.
+__device__ __forceinline__ u32x4 load16_in(const uint8_t* __restrict__ p, int n) {
+    const int by = n >= 16 ? 0 : 16 - n;
+    return move_down(*(const u32x4_byte*)(p - by), by < 16 ? by : 16);
 }
 
 // Four consecutive results of a row, the first n (>= 1) of which are in it.
@@ -149,303 +155,302 @@ __global__ __launch_bounds__(64 * WK) void k_block_few(const uint8_t* __restrict
     }
 }
 
-// Many rows.  The same product on blocks of 64 WM rows of the matrix (GRAD: its
-// columns) and 16 NT tokens; a wave has 64 of the rows and all of the tokens.
+// Many rows.  The same product on blocks of 256 rows of the matrix (GRAD: its
+// columns) and 16 NT tokens; each of four waves has 64 of the rows and all of the
+// tokens.
 //
-// A step takes 128 of the inner length.  The tokens' codes go to LDS by direct
-// loads one step ahead, 16-byte chunks XOR-swizzled by the token, and are read by
-// every wave; the matrix's come straight to operands (each wave has its own rows:
-// nothing to share), also one step ahead.  GRAD wants columns of the matrix: a
-// wave brings 128 rows by 64 columns to LDS and reads them transposed
-// (ds_read_b64_tr_b8: a lane receives one column of eight rows).  The scales of 32
-// steps lie in LDS.
+// A step takes 128 of the inner length.  What it needs, codes of the matrix and of
+// the tokens and their scales, comes to LDS by direct loads ST - 1 steps ahead.
+// Rows of 128 codes are XOR-swizzled by 16-byte chunks.  (Operands straight from
+// memory, 16 rows to an instruction, cost the texture path an access a lane: 217 us
+// for the case below.)  GRAD wants columns of the matrix: a wave brings 128 rows by
+// 64 columns and reads them transposed (ds_read_b64_tr_b8: a lane receives one
+// column of eight rows).
 //
-// DIRECT: the rows of x (GRAD: of the matrix too) start at 16-byte boundaries;
-// otherwise they are copied through registers, as is the last, partial step.
-constexpr int kTileScales = 32;
+// A wave runs alone on its SIMD, so nothing else hides its latencies: between the matrix instructions of a step stand the reads of the next
+// step's operands from LDS, the direct loads of a later one, and the scaling of
+// the results of two instructions before.
+//
+// DIRECT: rows of x and of the matrix start at 16-byte boundaries; otherwise codes
+// are copied through registers.
+constexpr int kTileWaves = 4, kTileThreads = 64 * kTileWaves, kTileRows = 64 * kTileWaves;
 
-template <bool V>
-struct Tag {
-    static constexpr bool value = V;
-};
-template <int V>
-struct Int {
-    static constexpr int value = V;
-};
+constexpr int kTileStages = 3;
 
-template <int WM, int NT, bool GRAD>
+template <int NT>
 struct BlockTile {
-    static constexpr int TT = 16 * NT, XROW = TT + 1;
-    static constexpr int X = TT * kBlock8;             // a stage of tokens
-    static constexpr int W = GRAD ? WM * 64 * kBlock8 : 0;  // and of the matrix
-    static constexpr int SX = 2 * (X + W), SW = SX + kTileScales * XROW * 4;
-    static constexpr int BYTES = SW + kTileScales * WM * 4;
+    static constexpr int TT = 16 * NT;
+    static constexpr int X = TT * kBlock8, W = kTileRows * kBlock8;  // codes of a step
+    static constexpr int SX = X + W;                                 // the tokens' scales: [16][NT]
+    static constexpr int SW = SX + (TT < 64 ? 64 : TT) * 4;          // the wave's block's scale, 64 times
+    static constexpr int STAGE = SW + kTileWaves * 256;
+    static constexpr int BYTES = kTileStages * STAGE;
+    static constexpr int LOADS = TT / 32 + 8 + 2;                    // a wave's direct loads of a step
 };
 
 // 16-byte chunk of row m (of 64 columns) that holds columns 16 c .. 16 c + 15: the
 // 32 rows that a transposing read touches spread over all banks.
 __device__ __forceinline__ int tile_chunk(int c, int m) { return c ^ ((m >> 2 & 1) ^ (m >> 4 & 3)); }
 
-template <typename O, int WM, int NT, bool GRAD, bool DIRECT>
-__global__ __launch_bounds__(64 * WM, 2) void k_block_tile(const uint8_t* __restrict__ x, const float* __restrict__ xs,
-                                                           int64_t S, const uint8_t* __restrict__ codes,
-                                                           const float* __restrict__ scales, int E, int64_t M,
-                                                           int64_t K, const int32_t* __restrict__ offsets,
-                                                           const int32_t* __restrict__ order, int64_t top,
-                                                           O* __restrict__ out) {
-    typedef BlockTile<WM, NT, GRAD> L;
+// What direct loads of codes behind a row's end read.
+__device__ const u32x4 g_no_codes = {0, 0, 0, 0};
+
+template <int V>
+struct Int {
+    static constexpr int value = V;
+};
+
+template <typename O, int NT, bool GRAD, bool DIRECT>
+__global__ __launch_bounds__(kTileThreads, 1) void k_block_tile(
+    const uint8_t* __restrict__ x, const float* __restrict__ xs, int64_t S, const uint8_t* __restrict__ codes,
+    const float* __restrict__ scales, int E, int64_t M, int64_t K, const int32_t* __restrict__ offsets,
+    const int32_t* __restrict__ order, int64_t top, O* __restrict__ out) {
+    typedef BlockTile<NT> L;
     typedef int i32x2 __attribute__((ext_vector_type(2)));
-    constexpr int TT = L::TT, NTHR = 64 * WM, R = 4;
-    constexpr int NX = TT * 8 / NTHR > 0 ? TT * 8 / NTHR : 1;  // a thread's chunks of a stage of tokens
+    constexpr int TT = L::TT, ST = kTileStages, R = 4, NX = TT / 32, NW = 8, NI = NT * R;
+    static_assert(NT % 2 == 0 && TT <= 128, "32 tokens to an instruction of every wave, scales by two waves");
     extern __shared__ __attribute__((aligned(16))) char s_mem[];
-    float* s_x = (float*)(s_mem + L::SX);  // [32][XROW]
-    float* s_w = (float*)(s_mem + L::SW);  // [32][WM]
     const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int r = lane & 15, q = lane >> 4;
     const Segment g = find_segment(offsets, S, E, TT, blockIdx.y);
     if (g.e < 0) return;
     const int64_t inner = GRAD ? M : K, outer = GRAD ? K : M, ib = blocks8(inner), kb = blocks8(K);
-    const int64_t o0 = ((int64_t)blockIdx.x * WM + w) * 64;  // the wave's rows
+    const int64_t o0 = (int64_t)blockIdx.x * kTileRows + w * 64;  // the wave's rows
     f32x4 acc[R][NT];
 #pragma unroll
     for (int a = 0; a < R; ++a)
 #pragma unroll
         for (int n = 0; n < NT; ++n) acc[a][n] = f32x4{0.f, 0.f, 0.f, 0.f};
+    uint32_t none = 0;  // bit n: token n 16 + r is a row of none
     if (g.e < E) {
-        const int64_t whole = inner / kBlock8;
         const uint8_t* wm = codes + (int64_t)g.e * M * K;
         const float* ws = scales + (int64_t)g.e * blocks8(M) * kb;
-        // a thread's chunks of tokens: 8 a token, chunk (lane & 7) ^ token at place lane & 7
-        const uint8_t* xp[NX];
+        auto source = [&](int t) { return source_row(order, top, S, g.p0 + (t < g.n ? t : g.n - 1)); };
+        // A thread's chunks of tokens: 8 a token, chunk (lane & 7) ^ token at place lane & 7, as
+        // 32-bit offsets from the segment's first row (with an order: from x's, whose rows are
+        // less than 4 GB then).
+        const uint8_t* xb = order ? x : x + g.p0 * inner;
+        uint32_t xo[NX];
         const int xc = ((tid & 7) ^ (tid >> 3 & 7)) * 16;
 #pragma unroll
         for (int i = 0; i < NX; ++i) {
-            const int t = (i * NTHR + tid) >> 3;
-            int64_t src = source_row(order, top, S, g.p0 + (t < g.n ? t : g.n - 1));
-            xp[i] = x + (src < 0 ? 0 : src) * inner + xc;
+            const int64_t src = source((i * kTileThreads + tid) >> 3);
+            xo[i] = (uint32_t)((order ? (src < 0 ? 0 : src) : src - g.p0) * inner) + xc;
         }
-        // forward: rows a 16 + r of the wave's 64, from its first one
+#pragma unroll
+        for (int n = 0; n < NT; ++n) none |= (order && source(n * 16 + r) < 0 ? 1u : 0u) << n;
+        // the token whose scale this lane fetches: place p of [16][NT]
+        const float* xsp;
+        {
+            int p = TT > 64 ? (w & 1) * 64 + lane : lane;
+            p = p < TT ? p : TT - 1;
+            const int64_t src = source(p % NT * 16 + p / NT);
+            xsp = xs + (src < 0 ? 0 : src) * ib;
+        }
+        const int64_t ob = (o0 < outer ? o0 : outer - 1) / kBlock8;
+        // Of the matrix, forward: rows of the wave like the tokens' (it reads no others'); GRAD:
+        // 16 rows of 64 columns an instruction, place lane & 3 of row m holding chunk
+        // tile_chunk(lane & 3, m).  Rows behind the last one read it.
         const uint8_t* wb = wm + (GRAD ? 0 : (o0 < outer ? o0 : outer - 1) * K);
-        uint32_t wo[R];
+        uint32_t wo[NW];
+        const int wrow = GRAD ? lane >> 2 : lane >> 3;
 #pragma unroll
-        for (int a = 0; a < R; ++a) {
-            const int64_t left = outer - 1 - o0;  // (rows past the last one read it)
-            wo[a] = (uint32_t)((a * 16 + r < left ? a * 16 + r : left < 0 ? 0 : left) * K) + q * 16;
-        }
-        auto xstage = [&](int b) { return s_mem + b * L::X; };
-        auto wstage = [&](int b) { return s_mem + 2 * L::X + b * L::W + w * (64 * kBlock8); };
-        // step st by direct loads: 1 KB an instruction
-        auto fill = [&](int64_t st, int b) {
-#pragma unroll
-            for (int i = 0; i < NX; ++i)
-                if (TT * 8 >= NTHR || tid < TT * 8) dma16_lane(xp[i] + st * kBlock8, xstage(b) + (i * NTHR + w * 64) * 16);
+        for (int i = 0; i < NW; ++i) {
             if constexpr (GRAD) {
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    // 16 rows of 64 columns; place lane & 3 of row m holds chunk tile_chunk(lane & 3, m)
-                    const int m = i * 16 + (lane >> 2), c = tile_chunk(lane & 3, m);
-                    const int64_t col = o0 + c * 16;
-                    dma16_lane(wm + (st * kBlock8 + m) * K + (col < outer ? col : outer - 16), wstage(b) + i * 1024);
+                const int64_t col = o0 + tile_chunk(lane & 3, i * 16 + wrow) * 16;
+                wo[i] = (uint32_t)((i * 16 + wrow) * K) + (uint32_t)(col < outer ? col : 0);
+            } else {
+                const int64_t left = outer - 1 - o0, row = i * 8 + wrow;
+                wo[i] = (uint32_t)((row < left ? row : left < 0 ? 0 : left) * K) + ((lane & 7) ^ (lane >> 3)) * 16;
+            }
+        }
+        auto wbase = [&](int64_t st) { return wb + st * kBlock8 * (GRAD ? K : 1); };
+        auto to_x = [&](int stage, int i) { return s_mem + stage * L::STAGE + (i * kTileThreads + w * 64) * 16; };
+        auto to_w = [&](int stage, int i) { return s_mem + stage * L::STAGE + L::X + w * (64 * kBlock8) + i * 1024; };
+        // direct load i of step st; LAST: of a step that the inner length ends in
+        auto load = [&](int64_t st, int stage, int i, auto last_tag) {
+            constexpr bool LAST = decltype(last_tag)::value;
+            const int left = (int)(inner - st * kBlock8);
+            if (i < NX) {
+                if constexpr (!DIRECT) return;
+                const uint8_t* b = xb + st * kBlock8;
+                if constexpr (LAST) dma16_lane(xc < left ? (const void*)(b + xo[i]) : (const void*)&g_no_codes, to_x(stage, i));
+                else dma16((const char*)b, xo[i], to_x(stage, i));
+            } else if (i < NX + NW) {
+                if constexpr (!DIRECT) return;
+                const int u = i - NX;
+                const uint8_t* b = wbase(st);
+                if constexpr (!LAST) {
+                    dma16((const char*)b, wo[u], to_w(stage, u));
+                } else if constexpr (GRAD) {
+                    // (rows behind the last one meet zeros of x)
+                    const int m = u * 16 + wrow;
+                    dma16_lane(b + wo[u] - (m < left ? 0 : (int64_t)(m - left + 1) * K), to_w(stage, u));
+                } else {
+                    dma16_lane(((lane & 7) ^ (lane >> 3)) * 16 < left ? (const void*)(b + wo[u]) : (const void*)&g_no_codes,
+                               to_w(stage, u));
                 }
+            } else if (i == NX + NW) {
+                dma4_lane(xsp + st, s_mem + stage * L::STAGE + L::SX + (TT > 64 ? (w & 1) * 256 : 0));
+            } else {
+                dma4_lane(GRAD ? ws + st * kb + ob : ws + ob * kb + st, s_mem + stage * L::STAGE + L::SW + w * 256);
             }
         };
-        // the same through registers: loads now, stores later.  LAST: the partial step.
-        auto copy_x = [&](int64_t st, u32x4 (&v)[NX], auto last_tag) {
+        // the same through registers: codes only
+        struct Copy {
+            u32x4 x[NX], w[NW];
+        };
+        auto copy = [&](int64_t st, Copy& c, auto last_tag) {
+            constexpr bool LAST = decltype(last_tag)::value;
             const int left = (int)(inner - st * kBlock8 < kBlock8 ? inner - st * kBlock8 : kBlock8);
 #pragma unroll
-            for (int i = 0; i < NX; ++i)
-                if (TT * 8 >= NTHR || tid < TT * 8) {
-                    if constexpr (decltype(last_tag)::value) v[i] = load16_end(xp[i] + st * kBlock8, left - xc, inner);
-                    else v[i] = *(const u32x4_byte*)(xp[i] + st * kBlock8);
-                }
-        };
-        auto keep_x = [&](int b, const u32x4 (&v)[NX]) {
-#pragma unroll
-            for (int i = 0; i < NX; ++i)
-                if (TT * 8 >= NTHR || tid < TT * 8) *(u32x4*)(xstage(b) + (i * NTHR + tid) * 16) = v[i];
-        };
-        // (columns behind the row's end hold the next row's and give results that are not
-        // stored; nothing behind the matrix is read)
-        auto copy_w = [&](int64_t st, u32x4 (&v)[8], auto last_tag) {
-            if constexpr (GRAD) {
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const int m = i * 16 + (lane >> 2), c = tile_chunk(lane & 3, m);
-                    const int64_t row = st * kBlock8 + m < M ? st * kBlock8 + m : M - 1, col = o0 + c * 16;
-                    if constexpr (decltype(last_tag)::value) {
-                        v[i] = load16_end(wm + row * K + (col < outer ? col : 0), (int)(outer - col < 16 ? outer - col : 16), K);
-                    } else {
-                        const int64_t at = row * K + (col < outer ? col : 0), over = at - (M * K - 16);
-                        v[i] = *(const u32x4_byte*)(wm + (over > 0 ? M * K - 16 : at));
-                        v[i] = move_down(v[i], over > 0 ? (int)over : 0);
-                    }
-                }
+            for (int i = 0; i < NX; ++i) {
+                const uint8_t* p = xb + st * kBlock8 + xo[i];
+                c.x[i] = LAST ? load16_in(p, left - xc) : *(const u32x4_byte*)p;
             }
-        };
-        auto keep_w = [&](int b, const u32x4 (&v)[8]) {
-            if constexpr (GRAD) {
 #pragma unroll
-                for (int i = 0; i < 8; ++i) *(u32x4*)(wstage(b) + i * 1024 + lane * 16) = v[i];
-            }
-        };
-        struct Part {
-            i32x8 v[R];
-        };
-        auto fetch = [&](int64_t st, Part& p) {
-            if constexpr (!GRAD) {
-                const uint8_t* b = wb + st * kBlock8;
-#pragma unroll
-                for (int a = 0; a < R; ++a)
-                    p.v[a] = join8(*(const u32x4_byte*)(b + wo[a]), *(const u32x4_byte*)(b + wo[a] + 64));
-            }
-        };
-        auto fetch_end = [&](int64_t st, Part& p) {
-            if constexpr (!GRAD) {
-                const uint8_t* b = wb + st * kBlock8;
-                const int left = (int)(inner - st * kBlock8) - q * 16;
-#pragma unroll
-                for (int a = 0; a < R; ++a)
-                    p.v[a] = join8(load16_end(b + wo[a], left, K), load16_end(b + wo[a] + 64, left - 64, K));
-            }
-        };
-        // the scales of the steps from st on
-        auto fill_scales = [&](int64_t st) {
-            for (int i = tid; i < TT * kTileScales; i += NTHR) {
-                const int t = i / kTileScales, j = i % kTileScales;
-                const int64_t src = source_row(order, top, S, g.p0 + (t < g.n ? t : g.n - 1));
-                if (st + j < ib) s_x[j * L::XROW + t] = src < 0 ? 0.f : xs[src * ib + st + j];
-            }
-            for (int i = tid; i < WM * kTileScales; i += NTHR) {
-                const int j = i / WM;
-                const int64_t o = ((int64_t)blockIdx.x * WM + i % WM) * 64, ob = (o < outer ? o : outer - 1) / kBlock8;
-                if (st + j < ib) s_w[i] = GRAD ? ws[(st + j) * kb + ob] : ws[ob * kb + st + j];
-            }
-        };
-        auto multiply = [&](int64_t st, int b, const Part& p) {
-            const int j = (int)(st % kTileScales);
-            const float sw = s_w[j * WM + w];
-            const char* xl = xstage(b);
-            i32x8 av[R];
-#pragma unroll
-            for (int a = 0; a < R; ++a) {
-                if constexpr (GRAD) {
-                    // rows q 16 + (0 .. 15) and 64 more of column a 16 + r: a lane fetches 8 bytes of
-                    // row r / 2 of eight, half r % 2 of the chunk
-                    const char* wl = wstage(b);
-#pragma unroll
-                    for (int f = 0; f < 4; ++f) {
-                        const int m = (f >> 1) * 64 + q * 16 + (f & 1) * 8 + (r >> 1);
-                        const i32x2 t = __builtin_amdgcn_ds_read_tr8_b64_v2i32(
-                            (__attribute__((address_space(3))) i32x2*)(wl + m * 64 + tile_chunk(a, m) * 16 + (r & 1) * 8));
-                        av[a][2 * f] = t[0];
-                        av[a][2 * f + 1] = t[1];
-                    }
+            for (int i = 0; i < NW; ++i) {
+                const uint8_t* p = wbase(st) + wo[i];
+                if constexpr (!LAST) {
+                    c.w[i] = *(const u32x4_byte*)p;
+                } else if constexpr (GRAD) {
+                    // columns behind the row's end hold the next row's and give results that are not
+                    // stored; nothing behind the matrix is read
+                    const int m = i * 16 + wrow;
+                    p -= m < left ? 0 : (int64_t)(m - left + 1) * K;
+                    c.w[i] = load16_in(p, (int)(wm + M * K - p < 16 ? wm + M * K - p : 16));
                 } else {
-                    av[a] = p.v[a];
+                    c.w[i] = load16_in(p, left - ((lane & 7) ^ (lane >> 3)) * 16);
                 }
             }
-            // a result is scaled and added two instructions after its own was issued; the next
-            // tokens are read while these are multiplied
-            auto tokens = [&](int n) {
-                const char* row = xl + (n * 16 + r) * kBlock8;
+        };
+        auto keep = [&](int stage, const Copy& c) {
+#pragma unroll
+            for (int i = 0; i < NX; ++i) *(u32x4*)(to_x(stage, i) + lane * 16) = c.x[i];
+#pragma unroll
+            for (int i = 0; i < NW; ++i) *(u32x4*)(to_w(stage, i) + lane * 16) = c.w[i];
+        };
+        auto fill = [&](int64_t st, int stage) {  // the whole step
+            st = st < ib ? st : ib - 1;
+#pragma unroll
+            for (int i = 0; i < L::LOADS; ++i) load(st, stage, i, Int<1>{});
+            if constexpr (!DIRECT) {
+                Copy c;
+                copy(st, c, Int<1>{});
+                keep(stage, c);
+            }
+        };
+        // operands of a step from its stage
+        auto matrix = [&](int stage, int a) {
+            const char* wl = s_mem + stage * L::STAGE + L::X + w * (64 * kBlock8);
+            if constexpr (GRAD) {
+                // rows q 16 + (0 .. 15) and 64 more of column a 16 + r: a lane fetches 8 bytes of
+                // row r / 2 of eight, half r % 2 of the chunk
+                i32x8 v;
+#pragma unroll
+                for (int f = 0; f < 4; ++f) {
+                    const int m = (f >> 1) * 64 + q * 16 + (f & 1) * 8 + (r >> 1);
+                    const i32x2 t = __builtin_amdgcn_ds_read_tr8_b64_v2i32(
+                        (__attribute__((address_space(3))) i32x2*)(wl + m * 64 + tile_chunk(a, m) * 16 + (r & 1) * 8));
+                    v[2 * f] = t[0];
+                    v[2 * f + 1] = t[1];
+                }
+                return v;
+            } else {
+                const char* row = wl + (a * 16 + r) * kBlock8;
                 return join8(*(const u32x4*)(row + ((q ^ (r & 7)) * 16)), *(const u32x4*)(row + (((q + 4) ^ (r & 7)) * 16)));
-            };
-            auto scale = [&](int n) { return sw * s_x[j * L::XROW + n * 16 + r]; };
+            }
+        };
+        auto tokens = [&](int stage, int n) {
+            const char* row = s_mem + stage * L::STAGE + (n * 16 + r) * kBlock8;
+            return join8(*(const u32x4*)(row + ((q ^ (r & 7)) * 16)), *(const u32x4*)(row + (((q + 4) ^ (r & 7)) * 16)));
+        };
+        struct Step {
+            i32x8 a[R], b[NT];
+            float sx[NT], sw;
+        };
+        auto read_scales = [&](int stage, Step& f) {
+            const float* sx = (const float*)(s_mem + stage * L::STAGE + L::SX) + r * NT;
+#pragma unroll
+            for (int n = 0; n < NT; ++n) f.sx[n] = sx[n];
+            f.sw = ((const float*)(s_mem + stage * L::STAGE + L::SW))[w * 64 + lane];
+        };
+        // One barrier a step: before it, this wave's loads of the next step have landed (those of
+        // later ones are still on their way) and its reads of this step are done.
+        auto landed = [&](auto ahead_tag) {
+            asm volatile("" ::: "memory");
+            __builtin_amdgcn_s_waitcnt(DIRECT ? vmcnt_imm(decltype(ahead_tag)::value * L::LOADS) & ~(15u << 8) : 0);
+            __builtin_amdgcn_s_barrier();
+            asm volatile("" ::: "memory");
+        };
+        Step f[2];
+        // part k of a step's operands: scales, rows, tokens
+        constexpr int PARTS = 1 + R + NT;
+        auto read = [&](int stage, Step& s, int k) {
+            if (k == 0) read_scales(stage, s);
+            else if (k <= R) s.a[k - 1] = matrix(stage, k - 1);
+            else s.b[k - 1 - R] = tokens(stage, k - 1 - R);
+        };
+        int now = 0, next = 1;  // stages of this step and the next
+        auto step = [&](int64_t st, auto c_tag, auto last_tag) {
+            constexpr int c = decltype(c_tag)::value;
+            landed(Int<ST - 2>{});
+            const int64_t far = st + ST < ib ? st + ST : ib - 1;
+            Copy cp;
+            if constexpr (!DIRECT) copy(far, cp, last_tag);
             f32x4 d[3];
-            i32x8 bv[2];
-            float sc[2];
-            bv[0] = tokens(0);
-            sc[0] = scale(0);
 #pragma unroll
-            for (int i = 0; i < NT * R + 2; ++i) {
-                const int n = i / R, a = i % R;
-                if (a == 0 && n + 1 < NT) bv[(n + 1) & 1] = tokens(n + 1);
-                if (a == 2 && n + 1 < NT) sc[(n + 1) & 1] = scale(n + 1);
-                if (i < NT * R) d[i % 3] = mfma8(av[a], bv[n & 1], f32x4{0.f, 0.f, 0.f, 0.f});
+            for (int i = 0; i < NI + 2; ++i) {
+                if (i < NI) d[i % 3] = mfma8(f[c].a[i % R], f[c].b[i / R], f32x4{0.f, 0.f, 0.f, 0.f});
+                __builtin_amdgcn_sched_barrier(0);
+                // the next step's operands and the direct loads of a later one, spread over this
+#pragma unroll
+                for (int k = 0; k < PARTS; ++k)
+                    if (i == 1 + k * (NI - 3) / PARTS) read(next, f[c ^ 1], k);
+#pragma unroll
+                for (int k = 0; k < L::LOADS; ++k)
+                    if (i == k * (NI - 1) / L::LOADS) load(far, now, k, last_tag);
+                __builtin_amdgcn_sched_barrier(0);
                 if (i >= 2) {
-                    const int m = (i - 2) / R, c = (i - 2) % R;
+                    const int n = (i - 2) / R, a = (i - 2) % R;
+                    if (a == 0) f[c].sx[n] *= f[c].sw;
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) acc[c][m][e] = fmaf(sc[m & 1], d[(i - 2) % 3][e], acc[c][m][e]);
+                    for (int e = 0; e < 4; ++e) acc[a][n][e] = fmaf(f[c].sx[n], d[(i - 2) % 3][e], acc[a][n][e]);
                 }
                 __builtin_amdgcn_sched_barrier(0);
             }
+            if constexpr (!DIRECT) keep(now, cp);
+            now = next;
+            next = next + 1 == ST ? 0 : next + 1;
         };
-        Part p[2];
-        if (whole > 0) {
-            fetch(0, p[0]);
-            if constexpr (DIRECT) {
-                fill(0, 0);
-            } else {
-                u32x4 xv[NX], wv[8];
-                copy_x(0, xv, Tag<false>{});
-                copy_w(0, wv, Tag<false>{});
-                keep_x(0, xv);
-                keep_w(0, wv);
-            }
-        }
-        // The step of buffer b; the next one is on its way meanwhile (the last is fetched
-        // twice rather than branched around: a branch here lets the compiler carry a step's
-        // results over it and spill).
-        auto step = [&](int64_t st, auto b_tag) {
-            constexpr int b = decltype(b_tag)::value;
-            if constexpr (DIRECT) __builtin_amdgcn_s_waitcnt(vmcnt_imm(0));  // this wave's direct loads, then everybody's
-            __syncthreads();
-            const int64_t next = st + 1 < whole ? st + 1 : st;
-            u32x4 xv[NX], wv[8];
-            fetch(next, p[b ^ 1]);
-            if constexpr (DIRECT) {
-                fill(next, b ^ 1);
-            } else {
-                copy_x(next, xv, Tag<false>{});
-                copy_w(next, wv, Tag<false>{});
-            }
-            multiply(st, b, p[b]);
-            if constexpr (!DIRECT) {
-                keep_x(b ^ 1, xv);
-                keep_w(b ^ 1, wv);
-            }
-        };
-        auto refill = [&](int64_t st) {
-            if (st % kTileScales == 0) {
-                if (st) __syncthreads();  // the old ones have been read
-                fill_scales(st);
-            }
-        };
+#pragma unroll
+        for (int i = 0; i < ST; ++i) fill(i, i);
+        landed(Int<ST - 1>{});
+#pragma unroll
+        for (int k = 0; k < PARTS; ++k) read(0, f[0], k);
+        // steps during which no loads of the last one begin, then the others
         int64_t st = 0;
-        for (; st + 1 < whole; st += 2) {
-            refill(st);
-            step(st, Int<0>{});
-            step(st + 1, Int<1>{});
+        for (; st + 1 + ST < ib - 1; st += 2) {
+            step(st, Int<0>{}, Int<0>{});
+            step(st + 1, Int<1>{}, Int<0>{});
         }
-        if (st < whole) {
-            refill(st);
-            step(st, Int<0>{});
+        for (; st + 1 < ib; st += 2) {
+            step(st, Int<0>{}, Int<1>{});
+            step(st + 1, Int<1>{}, Int<1>{});
         }
-        if (whole < ib) {
-            u32x4 xv[NX], wv[8];
-            copy_x(whole, xv, Tag<true>{});
-            copy_w(whole, wv, Tag<true>{});
-            fetch_end(whole, p[0]);
-            if constexpr (DIRECT) __builtin_amdgcn_s_waitcnt(vmcnt_imm(0));  // (the last fetch)
-            __syncthreads();
-            keep_x(0, xv);
-            keep_w(0, wv);
-            if (whole % kTileScales == 0) fill_scales(whole);
-            __syncthreads();
-            multiply(whole, 0, p[0]);
-        }
+        if (st < ib) step(st, Int<0>{}, Int<1>{});
+        __builtin_amdgcn_s_waitcnt(vmcnt_imm(0));  // (nothing writes to LDS behind the block's end)
     }
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
         const int t = n * 16 + r;
         if (t >= g.n) continue;
-        // (a row of none: zeros, whatever row 0 held)
-        const bool none = order && g.e < E && source_row(order, top, S, g.p0 + t) < 0;
+        const bool no = none >> n & 1;
 #pragma unroll
         for (int a = 0; a < R; ++a) {
             const int64_t o = o0 + a * 16 + q * 4;
             if (o < outer)
-                store_results<O>(out + (g.p0 + t) * outer + o, outer - o, none ? f32x4{0.f, 0.f, 0.f, 0.f} : acc[a][n]);
+                store_results<O>(out + (g.p0 + t) * outer + o, outer - o, no ? f32x4{0.f, 0.f, 0.f, 0.f} : acc[a][n]);
         }
     }
 }
@@ -461,25 +466,25 @@ static hipError_t block_launch(const BlockArgs& a, hipStream_t s) {
 #define KM_ARGS                                                                                                        \
     (const uint8_t*)a.x, a.x_scales, a.S, (const uint8_t*)a.codes, a.scales, (int)a.E, a.M, a.K, a.offsets, a.order,   \
         a.top, (O*)a.out
-#define KM_GO2(WM, NT, DIR)                                                                                            \
+#define KM_GO2(NT, DIR)                                                                                                \
     do {                                                                                                               \
-        constexpr int lds = BlockTile<WM, NT, GRAD>::BYTES;                                                            \
-        if (lds > 64 * 1024 &&                                                                                         \
-            (e = hipFuncSetAttribute((const void*)k_block_tile<O, WM, NT, GRAD, DIR>,                                  \
+        constexpr int lds = BlockTile<NT>::BYTES;                                                                      \
+        if ((e = hipFuncSetAttribute((const void*)k_block_tile<O, NT, GRAD, DIR>,                                      \
                                      hipFuncAttributeMaxDynamicSharedMemorySize, lds)) != hipSuccess)                  \
             return e;                                                                                                  \
-        hipLaunchKernelGGL((k_block_tile<O, WM, NT, GRAD, DIR>),                                                       \
-                           dim3((unsigned)((outer + 64 * WM - 1) / (64 * WM)),                                         \
+        hipLaunchKernelGGL((k_block_tile<O, NT, GRAD, DIR>),                                                           \
+                           dim3((unsigned)((outer + kTileRows - 1) / kTileRows),                                       \
                                 (unsigned)segment_tiles(a.S, a.E, a.offsets, 16 * NT)),                                \
-                           dim3(64 * WM), lds, s, KM_ARGS);                                                            \
+                           dim3(kTileThreads), lds, s, KM_ARGS);                                                       \
     } while (0)
-#define KM_GO(WM, NT)                      \
-    do {                                   \
-        if (direct) KM_GO2(WM, NT, true);  \
-        else KM_GO2(WM, NT, false);        \
+#define KM_GO(NT)                      \
+    do {                               \
+        if (direct) KM_GO2(NT, true);  \
+        else KM_GO2(NT, false);        \
     } while (0)
-    if (a.S >= 32 * a.E) {
-        KM_GO(4, 8);
+    // (copies through registers take 16 codes of a row, or of a matrix, at least)
+    if (a.S >= 32 * a.E && inner >= 16 && a.M * a.K >= 16) {
+        KM_GO(8);
         return hipGetLastError();
     }
 #undef KM_GO

@@ -105,6 +105,13 @@ __device__ __forceinline__ void dma16_lane(const void* from, const void* lds) {
                  : "memory");
 }
 
+// And of 4 bytes, to LDS word lds + 4 l.
+__device__ __forceinline__ void dma4_lane(const void* from, const void* lds) {
+    const uint32_t l = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) void*)lds;
+    asm volatile("s_nop 1\n\tglobal_load_lds_dword %0, off" ::"v"(from), "{m0}"(__builtin_amdgcn_readfirstlane(l))
+                 : "memory");
+}
+
 // Lanes of the wave whose v equals this lane's (among the lanes where
 // `active` holds): one ballot per bit of the values (0 <= v < 2^nbits).
 __device__ __forceinline__ uint64_t lanes_matching(int32_t v, int nbits, bool active) {
