@@ -81,22 +81,24 @@ __device__ __forceinline__ int64_t source_row(const int32_t* __restrict__ order,
     return o >= 0 && o < S ? o / (int32_t)top : -1;
 }
 
-// Few rows.  out = W x^T on 16 x 16 x 128 instructions, the matrix as A: a block
-// takes 16 rows of the matrix and 16 NT tokens, its WK waves every WK-th block
-// of 128 columns, whose sums are added in LDS in order.  Codes go from memory to
-// operands; GRAD reads the columns of the matrix byte by byte.
+// Any rows: few unaligned ones, and matrices too small for the other kernels.  out =
+// W x^T on 16 x 16 x 128 instructions, the matrix as A: a block takes 16 rows of the
+// matrix and 16 NT tokens, its WK waves every WK-th block of 128 columns, whose sums
+// are added in LDS in order.  Codes go from memory to operands; GRAD reads the
+// columns of the matrix byte by byte.  One row by 4096 x 4096: 6.8 us; 64 rows over
+// 16 experts of 4096 x 2048: 33 us, an access a lane in the texture path.
 template <typename O, int WK, int NT, bool GRAD>
 __global__ __launch_bounds__(64 * WK) void k_block_few(const uint8_t* __restrict__ x, const float* __restrict__ xs,
                                                        int64_t S, const uint8_t* __restrict__ codes,
                                                        const float* __restrict__ scales, int E, int64_t M, int64_t K,
                                                        const int32_t* __restrict__ offsets,
                                                        const int32_t* __restrict__ order, int64_t top,
-                                                       O* __restrict__ out) {
+                                                       int64_t y0, O* __restrict__ out) {
     constexpr int TT = 16 * NT;
     __shared__ f32x4 s_sum[WK][NT][64];
     const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int r = lane & 15, q = lane >> 4;
-    const Segment g = find_segment(offsets, S, E, TT, blockIdx.y);
+    const Segment g = find_segment(offsets, S, E, TT, (int)(y0 + blockIdx.y));
     if (g.e < 0) return;
     // inner: the length summed over; outer: the results of a row
     const int64_t inner = GRAD ? M : K, outer = GRAD ? K : M, ib = blocks8(inner), kb = blocks8(K);
@@ -156,8 +158,8 @@ __global__ __launch_bounds__(64 * WK) void k_block_few(const uint8_t* __restrict
 }
 
 // Many rows.  The same product on blocks of 256 rows of the matrix (GRAD: its
-// columns) and 16 NT tokens; each of four waves has 64 of the rows and all of the
-// tokens.
+// columns) and 16 NT tokens; each of its four waves has 64 of the rows and all of
+// the tokens.
 //
 // A step takes 128 of the inner length.  What it needs, codes of the matrix and of
 // the tokens and their scales, comes to LDS by direct loads ST - 1 steps ahead.
@@ -173,7 +175,7 @@ __global__ __launch_bounds__(64 * WK) void k_block_few(const uint8_t* __restrict
 //
 // DIRECT: rows of x and of the matrix start at 16-byte boundaries; otherwise codes
 // are copied through registers.
-constexpr int kTileWaves = 4, kTileThreads = 64 * kTileWaves, kTileRows = 64 * kTileWaves;
+constexpr int kTileThreads = 256, kTileRows = 256;
 
 constexpr int kTileStages = 3;
 
@@ -181,11 +183,12 @@ template <int NT>
 struct BlockTile {
     static constexpr int TT = 16 * NT;
     static constexpr int X = TT * kBlock8, W = kTileRows * kBlock8;  // codes of a step
-    static constexpr int SX = X + W;                                 // the tokens' scales: [16][NT]
-    static constexpr int SW = SX + (TT < 64 ? 64 : TT) * 4;          // the wave's block's scale, 64 times
-    static constexpr int STAGE = SW + kTileWaves * 256;
-    static constexpr int BYTES = kTileStages * STAGE;
-    static constexpr int LOADS = TT / 32 + 8 + 2;                    // a wave's direct loads of a step
+    static constexpr int SX = X + W;                         // the tokens' scales: [16][NT]
+    static constexpr int SW = SX + (TT < 64 ? 64 : TT) * 4;  // the scale of each wave's rows, 64 times
+    static constexpr int STAGE = SW + 4 * 256;
+    static constexpr int SRC = kTileStages * STAGE;          // the tokens' rows of x
+    static constexpr int BYTES = SRC + TT * 4;
+    static constexpr int LOADS = NT / 2 + 8 + 2;             // a wave's direct loads of a step
 };
 
 // 16-byte chunk of row m (of 64 columns) that holds columns 16 c .. 16 c + 15: the
@@ -204,11 +207,11 @@ template <typename O, int NT, bool GRAD, bool DIRECT>
 __global__ __launch_bounds__(kTileThreads, 1) void k_block_tile(
     const uint8_t* __restrict__ x, const float* __restrict__ xs, int64_t S, const uint8_t* __restrict__ codes,
     const float* __restrict__ scales, int E, int64_t M, int64_t K, const int32_t* __restrict__ offsets,
-    const int32_t* __restrict__ order, int64_t top, O* __restrict__ out) {
+    const int32_t* __restrict__ order, int64_t top, int64_t steps_per, O* __restrict__ out, float* __restrict__ part) {
     typedef BlockTile<NT> L;
     typedef int i32x2 __attribute__((ext_vector_type(2)));
-    constexpr int TT = L::TT, ST = kTileStages, R = 4, NX = TT / 32, NW = 8, NI = NT * R;
-    static_assert(NT % 2 == 0 && TT <= 128, "32 tokens to an instruction of every wave, scales by two waves");
+    constexpr int TT = L::TT, ST = kTileStages, R = 4, NX = NT / 2, NW = 8, NI = NT * R;
+    static_assert(NT % 2 == 0 && TT <= 128, "whole instructions of every wave, scales by two waves");
     extern __shared__ __attribute__((aligned(16))) char s_mem[];
     const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int r = lane & 15, q = lane >> 4;
@@ -221,35 +224,38 @@ __global__ __launch_bounds__(kTileThreads, 1) void k_block_tile(
     for (int a = 0; a < R; ++a)
 #pragma unroll
         for (int n = 0; n < NT; ++n) acc[a][n] = f32x4{0.f, 0.f, 0.f, 0.f};
-    uint32_t none = 0;  // bit n: token n 16 + r is a row of none
-    if (g.e < E) {
+    int32_t* s_src = (int32_t*)(s_mem + L::SRC);  // -1: a row of none
+    // the steps of this split of the inner length
+    const int64_t s0 = blockIdx.z * steps_per, s1 = s0 + steps_per < ib ? s0 + steps_per : ib;
+    if (g.e < E && s0 < s1) {
         const uint8_t* wm = codes + (int64_t)g.e * M * K;
         const float* ws = scales + (int64_t)g.e * blocks8(M) * kb;
-        auto source = [&](int t) { return source_row(order, top, S, g.p0 + (t < g.n ? t : g.n - 1)); };
-        // A thread's chunks of tokens: 8 a token, chunk (lane & 7) ^ token at place lane & 7, as
-        // 32-bit offsets from the segment's first row (with an order: from x's, whose rows are
-        // less than 4 GB then).
-        const uint8_t* xb = order ? x : x + g.p0 * inner;
-        uint32_t xo[NX];
+        if (tid < TT) s_src[tid] = (int32_t)source_row(order, top, S, g.p0 + (tid < g.n ? tid : g.n - 1));
+        __syncthreads();
+        // a thread's chunks of tokens: 8 a token, chunk (lane & 7) ^ token at place lane & 7
         const int xc = ((tid & 7) ^ (tid >> 3 & 7)) * 16;
+        // their rows of x (GRAD, whose rows follow each other: 32-bit offsets from the segment)
+        const uint8_t* xb = GRAD ? x + g.p0 * inner : x;
+        uint32_t xr[NX];
 #pragma unroll
         for (int i = 0; i < NX; ++i) {
-            const int64_t src = source((i * kTileThreads + tid) >> 3);
-            xo[i] = (uint32_t)((order ? (src < 0 ? 0 : src) : src - g.p0) * inner) + xc;
+            const int32_t src = s_src[(i * kTileThreads + tid) >> 3];
+            xr[i] = GRAD ? (uint32_t)((src - g.p0) * inner) + xc : src < 0 ? 0 : src;
         }
-#pragma unroll
-        for (int n = 0; n < NT; ++n) none |= (order && source(n * 16 + r) < 0 ? 1u : 0u) << n;
+        auto xp = [&](int64_t st, int i) {
+            return xb + st * kBlock8 + (GRAD ? (uint64_t)xr[i] : xc + (uint64_t)xr[i] * (uint32_t)inner);
+        };
         // the token whose scale this lane fetches: place p of [16][NT]
         const float* xsp;
         {
             int p = TT > 64 ? (w & 1) * 64 + lane : lane;
             p = p < TT ? p : TT - 1;
-            const int64_t src = source(p % NT * 16 + p / NT);
+            const int64_t src = s_src[p % NT * 16 + p / NT];
             xsp = xs + (src < 0 ? 0 : src) * ib;
         }
         const int64_t ob = (o0 < outer ? o0 : outer - 1) / kBlock8;
-        // Of the matrix, forward: rows of the wave like the tokens' (it reads no others'); GRAD:
-        // 16 rows of 64 columns an instruction, place lane & 3 of row m holding chunk
+        // Of the wave's rows of the matrix, instruction i.  Forward: 8 of them, like the tokens';
+        // GRAD: 16 rows of 64 columns, place lane & 3 of row m holding chunk
         // tile_chunk(lane & 3, m).  Rows behind the last one read it.
         const uint8_t* wb = wm + (GRAD ? 0 : (o0 < outer ? o0 : outer - 1) * K);
         uint32_t wo[NW];
@@ -273,9 +279,9 @@ __global__ __launch_bounds__(kTileThreads, 1) void k_block_tile(
             const int left = (int)(inner - st * kBlock8);
             if (i < NX) {
                 if constexpr (!DIRECT) return;
-                const uint8_t* b = xb + st * kBlock8;
-                if constexpr (LAST) dma16_lane(xc < left ? (const void*)(b + xo[i]) : (const void*)&g_no_codes, to_x(stage, i));
-                else dma16((const char*)b, xo[i], to_x(stage, i));
+                if constexpr (LAST) dma16_lane(xc < left ? (const void*)xp(st, i) : (const void*)&g_no_codes, to_x(stage, i));
+                else if constexpr (GRAD) dma16((const char*)(xb + st * kBlock8), xr[i], to_x(stage, i));
+                else dma16_lane(xp(st, i), to_x(stage, i));
             } else if (i < NX + NW) {
                 if constexpr (!DIRECT) return;
                 const int u = i - NX;
@@ -305,7 +311,7 @@ __global__ __launch_bounds__(kTileThreads, 1) void k_block_tile(
             const int left = (int)(inner - st * kBlock8 < kBlock8 ? inner - st * kBlock8 : kBlock8);
 #pragma unroll
             for (int i = 0; i < NX; ++i) {
-                const uint8_t* p = xb + st * kBlock8 + xo[i];
+                const uint8_t* p = xp(st, i);
                 c.x[i] = LAST ? load16_in(p, left - xc) : *(const u32x4_byte*)p;
             }
 #pragma unroll
@@ -331,7 +337,7 @@ __global__ __launch_bounds__(kTileThreads, 1) void k_block_tile(
             for (int i = 0; i < NW; ++i) *(u32x4*)(to_w(stage, i) + lane * 16) = c.w[i];
         };
         auto fill = [&](int64_t st, int stage) {  // the whole step
-            st = st < ib ? st : ib - 1;
+            st = s0 + st < s1 ? s0 + st : s1 - 1;
 #pragma unroll
             for (int i = 0; i < L::LOADS; ++i) load(st, stage, i, Int<1>{});
             if constexpr (!DIRECT) {
@@ -395,7 +401,7 @@ __global__ __launch_bounds__(kTileThreads, 1) void k_block_tile(
         auto step = [&](int64_t st, auto c_tag, auto last_tag) {
             constexpr int c = decltype(c_tag)::value;
             landed(Int<ST - 2>{});
-            const int64_t far = st + ST < ib ? st + ST : ib - 1;
+            const int64_t far = st + ST < s1 ? st + ST : s1 - 1;
             Copy cp;
             if constexpr (!DIRECT) copy(far, cp, last_tag);
             f32x4 d[3];
@@ -429,43 +435,324 @@ __global__ __launch_bounds__(kTileThreads, 1) void k_block_tile(
 #pragma unroll
         for (int k = 0; k < PARTS; ++k) read(0, f[0], k);
         // steps during which no loads of the last one begin, then the others
-        int64_t st = 0;
-        for (; st + 1 + ST < ib - 1; st += 2) {
+        int64_t st = s0;
+        for (; st + 1 + ST < s1 - 1; st += 2) {
             step(st, Int<0>{}, Int<0>{});
             step(st + 1, Int<1>{}, Int<0>{});
         }
-        for (; st + 1 < ib; st += 2) {
+        for (; st + 1 < s1; st += 2) {
             step(st, Int<0>{}, Int<1>{});
             step(st + 1, Int<1>{}, Int<1>{});
         }
-        if (st < ib) step(st, Int<0>{}, Int<1>{});
+        if (st < s1) step(st, Int<0>{}, Int<1>{});
         __builtin_amdgcn_s_waitcnt(vmcnt_imm(0));  // (nothing writes to LDS behind the block's end)
     }
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
         const int t = n * 16 + r;
         if (t >= g.n) continue;
-        const bool no = none >> n & 1;
+        const bool no = g.e < E && s0 < s1 && s_src[t] < 0;
 #pragma unroll
         for (int a = 0; a < R; ++a) {
             const int64_t o = o0 + a * 16 + q * 4;
-            if (o < outer)
-                store_results<O>(out + (g.p0 + t) * outer + o, outer - o, no ? f32x4{0.f, 0.f, 0.f, 0.f} : acc[a][n]);
+            if (o >= outer) continue;
+            const f32x4 v = no ? f32x4{0.f, 0.f, 0.f, 0.f} : acc[a][n];
+            const int64_t at = (g.p0 + t) * outer + o;
+            if (part) store_results<float>(part + blockIdx.z * S * outer + at, outer - o, v);
+            else store_results<O>(out + at, outer - o, v);
         }
     }
 }
 
-size_t block_product_scratch(int64_t, int64_t, int64_t, int64_t) { return 0; }
-size_t block_product_grad_scratch(int64_t, int64_t, int64_t, int64_t) { return 0; }
+// Few rows, aligned ones.  Each wave streams the columns of its own 16 R rows of
+// the matrix, and those of 16 NT tokens, through three slots of LDS by direct loads
+// of whole lines (straight to operands, 16 rows an instruction, the texture path
+// takes an access a lane: 32 us for the case below).  A block's WR x WK waves are
+// WR groups of rows; the WK waves of a group take every WK-th block of 128 columns,
+// and their sums are added in LDS in order.  Waves meet only there.
+constexpr int kStreamSlots = 3, kStreamScales = 8;
+
+template <int WR, int WK, int R, int NT>
+struct BlockStream {
+    static constexpr int SLOT = (R + NT) * 16 * kBlock8, LOADS = (R + NT) * 2;
+    static constexpr int RING = WR * WK * kStreamSlots * SLOT, SUMS = WK > 1 ? WR * WK * R * NT * 64 * 16 : 0;
+    static constexpr int BYTES = RING > SUMS ? RING : SUMS;
+};
+
+template <typename O, int WR, int WK, int R, int NT>
+__global__ __launch_bounds__(64 * WR * WK) void k_block_stream(
+    const uint8_t* __restrict__ x, const float* __restrict__ xs, int64_t S, const uint8_t* __restrict__ codes,
+    const float* __restrict__ scales, int E, int64_t M, int64_t K, const int32_t* __restrict__ offsets,
+    const int32_t* __restrict__ order, int64_t top, O* __restrict__ out) {
+    typedef BlockStream<WR, WK, R, NT> L;
+    constexpr int D = kStreamSlots, C = kStreamScales, TT = 16 * NT;
+    extern __shared__ __attribute__((aligned(16))) char s_mem[];
+    const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wr = w / WK, wk = w % WK, r = lane & 15, q = lane >> 4, row8 = lane >> 3;
+    const int at = ((lane & 7) ^ row8) * 16;  // the lane's chunk of a row: place lane & 7 holds chunk (lane & 7) ^ row
+    const Segment g = find_segment(offsets, S, E, TT, blockIdx.y);
+    if (g.e < 0) return;
+    const int64_t kb = blocks8(K), o0 = ((int64_t)blockIdx.x * WR + wr) * 16 * R;
+    f32x4 acc[R][NT];
+#pragma unroll
+    for (int a = 0; a < R; ++a)
+#pragma unroll
+        for (int n = 0; n < NT; ++n) acc[a][n] = f32x4{0.f, 0.f, 0.f, 0.f};
+    bool none[NT];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) none[n] = false;
+    if (g.e < E) {
+        const uint8_t* wm = codes + (int64_t)g.e * M * K + at;
+        const uint8_t *wp[2 * R], *xp[2 * NT];
+        const float* xsp[NT];
+#pragma unroll
+        for (int u = 0; u < 2 * R; ++u) {
+            const int64_t o = o0 + u * 8 + row8;
+            wp[u] = wm + (o < M ? o : M - 1) * K;
+        }
+        auto source = [&](int t) { return source_row(order, top, S, g.p0 + (t < g.n ? t : g.n - 1)); };
+#pragma unroll
+        for (int u = 0; u < 2 * NT; ++u) {
+            const int64_t src = source(u * 8 + row8);
+            xp[u] = x + (src < 0 ? 0 : src) * K + at;
+        }
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            const int64_t src = source(n * 16 + r);
+            none[n] = src < 0;
+            xsp[n] = xs + (src < 0 ? 0 : src) * kb;
+        }
+        const float* ws = scales + ((int64_t)g.e * blocks8(M) + (o0 < M ? o0 : M - 1) / kBlock8) * kb;
+        char* ring = s_mem + w * (D * L::SLOT);
+        const int64_t mine = wk < kb ? (kb - wk + WK - 1) / WK : 0;  // the wave's blocks: wk + WK i
+        auto fill = [&](int64_t i, int slot) {
+            const int64_t b = (wk + WK * i) * kBlock8;
+            const bool in = b + at < K;  // (a row's last block may hold fewer codes)
+#pragma unroll
+            for (int u = 0; u < 2 * R; ++u)
+                dma16_lane(in ? (const void*)(wp[u] + b) : (const void*)&g_no_codes, ring + slot * L::SLOT + u * 1024);
+#pragma unroll
+            for (int u = 0; u < 2 * NT; ++u)
+                dma16_lane(in ? (const void*)(xp[u] + b) : (const void*)&g_no_codes, ring + slot * L::SLOT + (2 * R + u) * 1024);
+        };
+        auto operand = [&](int slot, int tile) {
+            const char* row = ring + slot * L::SLOT + (tile * 16 + r) * kBlock8;
+            return join8(*(const u32x4*)(row + ((q ^ (r & 7)) * 16)), *(const u32x4*)(row + (((q + 4) ^ (r & 7)) * 16)));
+        };
+        for (int64_t c0 = 0; c0 < mine; c0 += C) {
+            const int n = mine - c0 < C ? (int)(mine - c0) : C;
+            float sx[C][NT], sw[C];
+#pragma unroll
+            for (int i = 0; i < C; ++i) {
+                const int64_t b = wk + WK * (c0 + (i < n ? i : n - 1));
+                sw[i] = ws[b];
+#pragma unroll
+                for (int t = 0; t < NT; ++t) sx[i][t] = xsp[t][b];
+            }
+#pragma unroll
+            for (int i = 0; i < D; ++i)
+                if (i < n) fill(c0 + i, i);
+#pragma unroll
+            for (int i = 0; i < C; ++i) {
+                if (i >= n) break;  // (uniform)
+                const int slot = i % D;
+                asm volatile("" ::: "memory");
+                if (i + D <= n) __builtin_amdgcn_s_waitcnt(vmcnt_imm((D - 1) * L::LOADS));
+                else __builtin_amdgcn_s_waitcnt(vmcnt_imm(0));
+                asm volatile("" ::: "memory");
+                i32x8 av[R], bv[NT];
+#pragma unroll
+                for (int a = 0; a < R; ++a) av[a] = operand(slot, a);
+#pragma unroll
+                for (int t = 0; t < NT; ++t) bv[t] = operand(slot, R + t);
+                asm volatile("" ::: "memory");
+                __builtin_amdgcn_s_waitcnt(vmcnt_imm(63) & ~(15u << 8));  // read, then filled again
+                asm volatile("" ::: "memory");
+                if (i + D < n) fill(c0 + i + D, slot);
+#pragma unroll
+                for (int t = 0; t < NT; ++t) {
+                    const float s = sw[i] * sx[i][t];
+#pragma unroll
+                    for (int a = 0; a < R; ++a) {
+                        const f32x4 d = mfma8(av[a], bv[t], f32x4{0.f, 0.f, 0.f, 0.f});
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) acc[a][t][e] = fmaf(s, d[e], acc[a][t][e]);
+                    }
+                }
+            }
+        }
+    }
+    auto store = [&](int row, int a, int t, int l, f32x4 v) {
+        const int tk = t * 16 + (l & 15);
+        const int64_t o = ((int64_t)blockIdx.x * WR + row) * 16 * R + a * 16 + (l >> 4) * 4;
+        if (tk < g.n && o < M) store_results<O>(out + (g.p0 + tk) * M + o, M - o, v);
+    };
+#pragma unroll
+    for (int a = 0; a < R; ++a)
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+            if (none[t]) acc[a][t] = f32x4{0.f, 0.f, 0.f, 0.f};
+            if constexpr (WK == 1) store(wr, a, t, lane, acc[a][t]);
+        }
+    if constexpr (WK > 1) {
+        __syncthreads();  // every wave is done with its slots
+        f32x4* sums = (f32x4*)s_mem;  // [WR][WK][R][NT][64]
+        constexpr int PER = R * NT * 64;
+#pragma unroll
+        for (int a = 0; a < R; ++a)
+#pragma unroll
+            for (int t = 0; t < NT; ++t) sums[((w * R + a) * NT + t) * 64 + lane] = acc[a][t];
+        __syncthreads();
+        for (int i = threadIdx.x; i < WR * PER; i += 64 * WR * WK) {
+            const int row = i / PER, rest = i % PER;
+            f32x4 v = sums[row * WK * PER + rest];
+#pragma unroll
+            for (int k = 1; k < WK; ++k) v += sums[(row * WK + k) * PER + rest];
+            store(row, rest / (64 * NT), rest / 64 % NT, rest & 63, v);
+        }
+    }
+}
+
+// out[i] = the sum of nsplit partial sums, in order; four elements a thread.
+template <typename O>
+__global__ __launch_bounds__(256) void k_block_join(const float* __restrict__ part, int64_t n, int nsplit,
+                                                    O* __restrict__ out, int64_t block0) {
+    typedef f32x4 f32x4_any __attribute__((aligned(4)));
+    const int64_t i = ((block0 + blockIdx.x) * 256 + threadIdx.x) * 4;
+    if (i >= n) return;
+    if (i + 4 <= n) {
+        f32x4 a = *(const f32x4_any*)(part + i);
+        for (int s = 1; s < nsplit; ++s) a += *(const f32x4_any*)(part + s * n + i);
+        store_results<O>(out + i, 4, a);
+    } else {
+        for (int64_t j = i; j < n; ++j) {
+            float a = part[j];
+            for (int s = 1; s < nsplit; ++s) a += part[s * n + j];
+            out[j] = elem_from<O>(a);
+        }
+    }
+}
+
+// How a product is launched: token tiles of a block (0: not the kernel of many rows)
+// and splits of the inner length, or the waves of a group in the kernel of few
+// aligned rows (0: not that one), by the time each would take, us:
+//   many rows   rounds of 256 blocks (one for each compute unit) of (steps of a
+//               split x step + 4), a step 0.46, 0.6, 0.95 for 2, 4, 8 token tiles
+//               and at least 1.05 where the matrices come from memory (64 MB or
+//               more); splits add 4 and their sums' way through memory
+//   few rows    3 + the matrices once for every 16 tokens at 11 TB/s, a fifth more
+//               where an expert has several such tiles
+//   both        no less than the matrices take from memory, 5.1 TB/s
+// Measured (bf16; 17: four waves a group, 18: two, 24: one; nt / splits; the last
+// column: the rule's choice), us a call in a graph:
+//   rows, matrices        17     18     24    2/1    2/2    2/4    4/1    4/2    8/1    8/2   rule
+//      1, 4096 x 4096    7.5   10.3   16.1   17.9          10.8   20.9                      10: 6.4
+//     64, 4096 x 4096   10.9   11.5   17.7   18.9          13.6   23.7                       17
+//    256, 4096 x 4096   32.7   27.2   23.9   19.0   20.3   22.9   23.3   22.0   33.9   28.6  2/1
+//   1024, 4096 x 4096  116.0   97.1   85.3   39.6   53.5   76.5   27.4   42.9   35.0   35.4  4/1
+//   4096, 4096 x 4096  463.7  364.6  323.0  141.2  202.8  325.5  100.4  154.3   83.3  128.5  8/1
+//     64, 16 4096 x 2048 29.6  27.4   25.5   29.2          43.2   29.3                       24
+//    128, 8 4096 x 4096 37.8   36.8   39.5   38.2   32.5   46.0   38.7   32.6   40.5   34.5  2/2
+//    512, 8 of those    77.6   69.4   69.6   57.5   58.5   66.9   43.9   49.6   47.3   39.7  8/2
+//   4096, 8 of those   487.3  398.2  361.9  200.4  270.4  366.9  141.6  198.8  120.5  160.0  8/1
+// The gradient (no kernel of few rows):
+//     16, 4096 x 4096                         22.9   17.1   13.9   23.7   17.8   31.0   21.9  2/8: 13.4
+//    512, 4096 x 4096                         24.9   35.8   50.8   27.6   25.5   35.6   30.3  2/1
+//    512, 8 4096 x 4096                       70.3   67.2   74.9   47.6   55.2   50.9   42.6  8/2
+//   2048, 8 4096 x 2048                       66.5   80.1  118.5   52.1   62.4   38.1   56.6  8/1
+struct BlockShape {
+    int nt;
+    int64_t splits;
+    int waves;
+};
+static BlockShape block_shape(bool grad, bool direct, int64_t S, int64_t E, int64_t M, int64_t K) {
+    const int64_t inner = grad ? M : K, outer = grad ? K : M, steps = blocks8(inner);
+    BlockShape best{0, 1, 0};
+    // (the copies of unaligned rows through registers take 16 codes of a row, or of a matrix, at least)
+    if (!direct && (inner < 16 || M * K < 16)) return best;
+    const int64_t live = S < E ? S : E;
+    if (live < 1) return best;
+    // an expert's last tile is half full on average
+    auto tiles = [&](int64_t tt) {
+        const int64_t half = S / tt + (live + 1) / 2;
+        return E == 1 ? (S + tt - 1) / tt : half > live ? half : live;
+    };
+    const double bytes = (double)live * (double)M * (double)K, memory = bytes / 5.1e6;
+    double least = 1e30;
+    const double step_us[3] = {0.46, 0.6, 0.95};
+    for (int i = 0; i < 3; ++i) {
+        const int64_t blocks = (outer + kTileRows - 1) / kTileRows * tiles(32 << i);
+        const double step = bytes >= 64e6 && step_us[i] < 1.05 ? 1.05 : step_us[i];
+        for (int64_t n = 1; n <= 16 && (n == 1 || steps / n >= 2); n *= 2) {
+            const double rounds = (double)((blocks * n + 255) / 256), loop = rounds * (double)((steps + n - 1) / n) * step;
+            double us = (loop > memory ? loop : memory) + 4.0 * rounds;
+            if (n > 1) us += 4.0 + (double)(2 * n * S * outer) * sizeof(float) / 3.8e6;
+            if (us < least) {
+                least = us;
+                best = {2 << i, n, 0};
+            }
+        }
+    }
+    // (the token tiles of a launch: 65535 at most)
+    if (!grad && direct && S <= (int64_t)1 << 15) {
+        const int64_t t16 = tiles(16), groups = (M + 31) / 32 * t16;
+        const double read = (double)t16 * (double)M * (double)K / 1.1e7;
+        const double us = 3.0 + (read > memory ? read : memory) * (t16 > live ? 1.2 : 1.0);
+        if (us < least) best = {0, 1, (M + 15) / 16 * t16 <= 256 ? 8 : groups <= 512 ? 4 : groups < 2048 ? 2 : 1};
+    }
+    return best;
+}
+
+// (the workspace is asked for by sizes alone: enough for unaligned rows too)
+static size_t block_scratch(bool grad, int64_t S, int64_t E, int64_t M, int64_t K) {
+    const int64_t a = block_shape(grad, true, S, E, M, K).splits, b = block_shape(grad, false, S, E, M, K).splits;
+    const int64_t n = a > b ? a : b;
+    return n > 1 ? ((size_t)(n * S * (grad ? K : M)) * sizeof(float) + 255) & ~(size_t)255 : 0;
+}
+size_t block_product_scratch(int64_t S, int64_t E, int64_t M, int64_t K) { return block_scratch(false, S, E, M, K); }
+size_t block_product_grad_scratch(int64_t S, int64_t E, int64_t M, int64_t K) { return block_scratch(true, S, E, M, K); }
 
 template <typename O, bool GRAD>
-static hipError_t block_launch(const BlockArgs& a, hipStream_t s) {
+static hipError_t block_launch(const BlockArgs& a, void* ws, hipStream_t s) {
     const int64_t inner = GRAD ? a.M : a.K, outer = GRAD ? a.K : a.M;
-    const bool direct = inner % 16 == 0 && (uintptr_t)a.x % 16 == 0 && (!GRAD || (a.K % 16 == 0 && (uintptr_t)a.codes % 16 == 0));
+    const bool direct = inner % 16 == 0 && (uintptr_t)a.x % 16 == 0 && (uintptr_t)a.codes % 16 == 0 && a.K % 16 == 0;
+    const BlockShape shape = block_shape(GRAD, direct, a.S, a.E, a.M, a.K);
     hipError_t e = hipSuccess;
-#define KM_ARGS                                                                                                        \
-    (const uint8_t*)a.x, a.x_scales, a.S, (const uint8_t*)a.codes, a.scales, (int)a.E, a.M, a.K, a.offsets, a.order,   \
-        a.top, (O*)a.out
+    if constexpr (!GRAD) {
+#define KM_ST(WR, WK, R, NT)                                                                                            \
+    do {                                                                                                                \
+        constexpr int lds = BlockStream<WR, WK, R, NT>::BYTES;                                                          \
+        if ((e = hipFuncSetAttribute((const void*)k_block_stream<O, WR, WK, R, NT>,                                     \
+                                     hipFuncAttributeMaxDynamicSharedMemorySize, lds)) != hipSuccess)                   \
+            return e;                                                                                                   \
+        hipLaunchKernelGGL((k_block_stream<O, WR, WK, R, NT>),                                                          \
+                           dim3((unsigned)((a.M + 16 * WR * R - 1) / (16 * WR * R)),                                    \
+                                (unsigned)segment_tiles(a.S, a.E, a.offsets, 16 * NT)),                                 \
+                           dim3(64 * WR * WK), lds, s, (const uint8_t*)a.x, a.x_scales, a.S, (const uint8_t*)a.codes,   \
+                           a.scales, (int)a.E, a.M, a.K, a.offsets, a.order, a.top, (O*)a.out);                         \
+        return hipGetLastError();                                                                                       \
+    } while (0)
+        switch (shape.waves) {
+            case 8: KM_ST(1, 8, 1, 1);
+            case 4: KM_ST(1, 4, 2, 1);
+            case 2: KM_ST(2, 2, 2, 1);
+            case 1: KM_ST(4, 1, 2, 1);
+            default: break;
+        }
+#undef KM_ST
+    }
+    if (shape.nt == 0) {
+        // (the grid's second axis holds 65535 token tiles)
+        const int64_t all = segment_tiles(a.S, a.E, a.offsets, 16), most = 1 << 15;
+        for (int64_t y0 = 0; y0 < all; y0 += most)
+            hipLaunchKernelGGL((k_block_few<O, 8, 1, GRAD>),
+                               dim3((unsigned)((outer + 15) / 16), (unsigned)(all - y0 < most ? all - y0 : most)), dim3(512), 0,
+                               s, (const uint8_t*)a.x, a.x_scales, a.S, (const uint8_t*)a.codes, a.scales, (int)a.E, a.M,
+                               a.K, a.offsets, a.order, a.top, y0, (O*)a.out);
+        return hipGetLastError();
+    }
+    const int64_t steps = blocks8(inner), per = (steps + shape.splits - 1) / shape.splits;
+    float* part = shape.splits > 1 ? (float*)ws : nullptr;
 #define KM_GO2(NT, DIR)                                                                                                \
     do {                                                                                                               \
         constexpr int lds = BlockTile<NT>::BYTES;                                                                      \
@@ -474,31 +761,31 @@ static hipError_t block_launch(const BlockArgs& a, hipStream_t s) {
             return e;                                                                                                  \
         hipLaunchKernelGGL((k_block_tile<O, NT, GRAD, DIR>),                                                           \
                            dim3((unsigned)((outer + kTileRows - 1) / kTileRows),                                       \
-                                (unsigned)segment_tiles(a.S, a.E, a.offsets, 16 * NT)),                                \
-                           dim3(kTileThreads), lds, s, KM_ARGS);                                                       \
+                                (unsigned)segment_tiles(a.S, a.E, a.offsets, 16 * NT), (unsigned)shape.splits),        \
+                           dim3(kTileThreads), lds, s, (const uint8_t*)a.x, a.x_scales, a.S, (const uint8_t*)a.codes,  \
+                           a.scales, (int)a.E, a.M, a.K, a.offsets, a.order, a.top, per, (O*)a.out, part);             \
     } while (0)
 #define KM_GO(NT)                      \
     do {                               \
         if (direct) KM_GO2(NT, true);  \
         else KM_GO2(NT, false);        \
     } while (0)
-    // (copies through registers take 16 codes of a row, or of a matrix, at least)
-    if (a.S >= 32 * a.E && inner >= 16 && a.M * a.K >= 16) {
-        KM_GO(8);
-        return hipGetLastError();
-    }
+    if (shape.nt == 8) KM_GO(8);
+    else if (shape.nt == 4) KM_GO(4);
+    else KM_GO(2);
 #undef KM_GO
 #undef KM_GO2
-    hipLaunchKernelGGL((k_block_few<O, 8, 1, GRAD>),
-                       dim3((unsigned)((outer + 15) / 16), (unsigned)segment_tiles(a.S, a.E, a.offsets, 16)), dim3(512),
-                       0, s, KM_ARGS);
-#undef KM_ARGS
+    if ((e = hipGetLastError()) != hipSuccess || !part) return e;
+    const int64_t n = a.S * outer;
+    in_launches((n + 1023) / 1024, [&](int64_t b0, unsigned nb) {
+        hipLaunchKernelGGL((k_block_join<O>), dim3(nb), dim3(256), 0, s, part, n, (int)shape.splits, (O*)a.out, b0);
+    });
     return hipGetLastError();
 }
 
 hipError_t launch_block_product(DType ot, bool grad, const BlockArgs& a, void* ws, hipStream_t s) {
     if (a.S == 0) return hipSuccess;
-#define KM_GO(O) return grad ? block_launch<O, true>(a, s) : block_launch<O, false>(a, s)
+#define KM_GO(O) return grad ? block_launch<O, true>(a, ws, s) : block_launch<O, false>(a, ws, s)
     if (ot == DType::F32) KM_GO(float);
     if (ot == DType::F16) KM_GO(_Float16);
     KM_GO(uint16_t);

@@ -105,6 +105,12 @@ SHAPES = [  # S, E, M, K, kind of offsets
     (1000, 5, 260, 400, "first"), (1300, 3, 520, 160, "last"), (2000, 7, 264, 144, "tail"), (40, 40, 48, 80, "even"),
     (200, 100, 33, 65, "tail"), (3000, 2, 128, 128, "even"), (0, 2, 64, 64, "even"), (600, 4, 1024, 1024, "even"),
     (4500, 3, 1536, 256, "even"), (2100, 2, 2304, 640, "tail"),
+    # every kernel of few rows, every token tile with and without splits, aligned and not
+    (1, 1, 4096, 1024, "even"), (2, 1, 8192, 384, "even"), (64, 1, 2048, 1024, "even"), (100, 3, 4096, 512, "tail"),
+    (200, 8, 8192, 256, "even"), (150, 1, 2048, 1024, "even"), (520, 2, 1024, 2048, "tail"), (1100, 1, 4096, 640, "even"),
+    (2100, 1, 2048, 2048, "even"), (300, 1, 260, 4096, "even"), (130, 1, 4097, 257, "even"), (600, 1, 513, 2049, "even"),
+    (40, 1, 700, 2050, "even"), (3000, 1, 1030, 1031, "even"), (9, 2, 15, 9, "even"), (70000, 2, 3, 5, "tail"),
+    (1, 1, 40, 40000, "even"), (1, 1, 40000, 40, "even"), (33000, 1, 16, 32, "even"),
 ]
 
 
