@@ -161,16 +161,22 @@ __global__ __launch_bounds__(64 * WPR) void k_norm_grad(const T* __restrict__ gr
     __shared__ float s_sum[2][2 * WPR];
     const int w = threadIdx.x >> 6, lane = threadIdx.x & 63;
     const int c0 = lane + 64 * w;
-    float wv[NC][N], acc[NC][N];
+    // four chunks' weights are read again for every row: kept, they would cost registers
+    // that the rows need (spilled, two rows of 14016 took 34 us)
+    constexpr bool KEEP = NC < 4;
+    float wv[KEEP ? NC : 1][N], acc[NC][N];
+    auto weights = [&](int i, float (&v)[N]) {
+        const int c = c0 + 64 * WPR * i;
+        if (c < C) load_weight<T>(weight, wide, chunk_at<T>(c, d), d, v);
+#pragma unroll
+        for (int j = 0; j < N; ++j)
+            if (c >= C) v[j] = 0.f;
+    };
 #pragma unroll
     for (int i = 0; i < NC; ++i) {
-        const int c = c0 + 64 * WPR * i, e0 = chunk_at<T>(c, d);
-        if (c < C) load_weight<T>(weight, wide, e0, d, wv[i]);
+        if constexpr (KEEP) weights(i, wv[i]);
 #pragma unroll
-        for (int j = 0; j < N; ++j) {
-            if (c >= C) wv[i][j] = 0.f;
-            acc[i][j] = 0.f;
-        }
+        for (int j = 0; j < N; ++j) acc[i][j] = 0.f;
     }
     const float dd = (float)d;
     int par = 0;
@@ -190,9 +196,10 @@ __global__ __launch_bounds__(64 * WPR) void k_norm_grad(const T* __restrict__ gr
 #pragma unroll
         for (int i = 0; i < NC; ++i) {
             const int c = c0 + 64 * WPR * i, skip = c * N - chunk_at<T>(c, d);
+            if constexpr (!KEEP) weights(i, wv[0]);
 #pragma unroll
             for (int j = 0; j < N; ++j) {
-                const float hj = elem_f32(hv[i][j]), u = elem_f32(gv[i][j]) * wv[i][j];
+                const float hj = elem_f32(hv[i][j]), u = elem_f32(gv[i][j]) * wv[KEEP ? i : 0][j];
                 if (j >= skip) {
                     hh = fmaf(hj, hj, hh);
                     uh = fmaf(u, hj, uh);
@@ -215,11 +222,15 @@ __global__ __launch_bounds__(64 * WPR) void k_norm_grad(const T* __restrict__ gr
         for (int i = 0; i < NC; ++i) {
             const int c = c0 + 64 * WPR * i, e0 = chunk_at<T>(c, d);
             if (c >= C) continue;
+            if constexpr (!KEEP) {
+                weights(i, wv[0]);
+                asm("" : "+v"(gv[i]), "+v"(hv[i]));  // (converted again, not kept as float32)
+            }
             float o[N];
 #pragma unroll
             for (int j = 0; j < N; ++j) {
                 const float hj = elem_f32(hv[i][j]), g = elem_f32(gv[i][j]);
-                o[j] = fmaf(r, g * wv[i][j], -hj * k);
+                o[j] = fmaf(r, g * wv[KEEP ? i : 0][j], -hj * k);
                 if (gres) o[j] += elem_f32(rv[i][j]);
                 if (GW) acc[i][j] = fmaf(g, hj * r, acc[i][j]);
             }
@@ -293,6 +304,7 @@ hipError_t launch_norm_grad(DType xt, const void* grad, const void* h, int64_t T
         else if (C <= 256) KM_GO2(TT, 4, 1);   \
         else if (C <= 512) KM_GO2(TT, 4, 2);   \
         else if (C <= 1024) KM_GO2(TT, 4, 4);  \
+        else if (C <= 2048) KM_GO2(TT, 16, 2); \
         else KM_GO2(TT, 16, 4);                \
     } while (0)
         if (xt == DType::F32) KM_GO(float);

@@ -204,6 +204,26 @@ def test_norm_grad(km, dtype, T, d):
         _near(gw, wgw, U[weight.dtype] * wgw.abs() + (T + 96) * U32 * size + TINY[weight.dtype], "grad_weight")
 
 
+@pytest.mark.parametrize("dtype,T,d", [(torch.bfloat16, 3, 32768), (torch.float16, 2, 20001), (torch.float32, 2, 12345),
+                                       (torch.bfloat16, 1500, 16384), (torch.bfloat16, 1100, 8200)])
+def test_long_rows(km, dtype, T, d):
+    # (a lane's sums are longer: 64 terms more, and as many more rows a block)
+    g, h, w = _rows((T, d), dtype, 1, 0.3), _rows((T, d), dtype, 2), (1.0 + 0.2 * _rows((d,), torch.float32, 3)).to(dtype)
+    gx, gw = km.kmeans_norm_grad(g, h, w, 1e-5)
+    hd, gd = h.double(), g.double()
+    r = 1.0 / (hd.square().mean(1, keepdim=True) + 1e-5).sqrt()
+    u = gd * w.double()
+    want = r * u - hd * r ** 3 * (u * hd).mean(1, keepdim=True)
+    size = (r * u).abs() + hd.abs() * r ** 3 * (u * hd).abs().mean(1, keepdim=True)
+    _near(gx, want, U[dtype] * want.abs() + 384 * U32 * size + TINY[dtype], "grad_x")
+    wgw, size = (gd * hd * r).sum(0), (gd * hd * r).abs().sum(0)
+    _near(gw, wgw, U[dtype] * wgw.abs() + (T + 160) * U32 * size + TINY[dtype], "grad_weight")
+    y, _ = km.kmeans_norm(h, w, 1e-5)
+    _near(y, hd * r * w.double(), (U[dtype] + 96 * U32) * (hd * r * w.double()).abs() + TINY[dtype], "y")
+    q, s, _ = km.kmeans_norm_quantize(h, w, 1e-5)
+    _check_codes(q, s, hd * r * w.double(), 96 * U32, "codes")
+
+
 def test_grad_by_differences(km):
     # along a direction v: (f(h + e v) - f(h - e v)) / 2 e of f = <g, y>, in float32 sums of
     # 40 x 160 terms of size 1 (off by 6400 u32 / 2 e = 0.02 at e = 1/100) and a third-order
