@@ -52,7 +52,7 @@ __device__ __forceinline__ uint32_t magnitude(float v) { return __float_as_uint(
 // so that its inverse is finite; an infinite or NaN block keeps an infinite or
 // NaN scale, and then all its values are NaN.
 __device__ __forceinline__ float block_scale(uint32_t amax) {
-    const float s = __uint_as_float(amax) / 448.f;
+    const float s = __uint_as_float(amax) * (1.f / 448.f);
     return s < 0x1p-100f ? 0x1p-100f : s;
 }
 

@@ -430,7 +430,8 @@ KM_API km_status kmeans_codes_product_grad(const void *grad, km_dtype xt, int64_
  */
 
 /* 8-bit codes of a matrix by blocks of `rows` x 128 elements.
- *   scale = max(amax / 448, 2^-100), amax the block's largest magnitude,
+ *   scale = max(amax * (1 / 448), 2^-100) in float32, amax the block's largest
+ *           magnitude,
  *   code  = x / scale, rounded to nearest even (from its float32 quotient).
  * A block that holds an infinity or a NaN has values that are all NaN.
  *   x       [B,M,K] of dtype xt.
