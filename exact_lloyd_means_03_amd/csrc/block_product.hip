@@ -184,7 +184,7 @@ struct BlockTile {
     static constexpr int TT = 16 * NT;
     static constexpr int X = TT * kBlock8, W = kTileRows * kBlock8;  // codes of a step
     static constexpr int SX = X + W;                         // the tokens' scales: [16][NT]
-    static constexpr int SW = SX + (TT < 64 ? 64 : TT) * 4;  // the scale of each wave's rows, 64 times
+    static constexpr int SW = SX + (TT + 63) / 64 * 256;     // the scale of each wave's rows, 64 times
     static constexpr int STAGE = SW + 4 * 256;
     static constexpr int SRC = kTileStages * STAGE;          // the tokens' rows of x
     static constexpr int BYTES = SRC + TT * 4;
@@ -197,11 +197,6 @@ __device__ __forceinline__ int tile_chunk(int c, int m) { return c ^ ((m >> 2 & 
 
 // What direct loads of codes behind a row's end read.
 __device__ const u32x4 g_no_codes = {0, 0, 0, 0};
-
-template <int V>
-struct Int {
-    static constexpr int value = V;
-};
 
 template <typename O, int NT, bool GRAD, bool DIRECT>
 __global__ __launch_bounds__(kTileThreads, 1) void k_block_tile(
@@ -637,8 +632,8 @@ __global__ __launch_bounds__(256) void k_block_join(const float* __restrict__ pa
 // and splits of the inner length, or the waves of a group in the kernel of few
 // aligned rows (0: not that one), by the time each would take, us:
 //   many rows   rounds of 256 blocks (one for each compute unit) of (steps of a
-//               split x step + 4), a step 0.46, 0.6, 0.95 for 2, 4, 8 token tiles
-//               and at least 1.05 where the matrices come from memory (64 MB or
+//               split x step + 4), a step 0.46, 0.6, 0.78, 0.95 for 2, 4, 6, 8 token
+//               tiles and at least 1.05 where the matrices come from memory (64 MB or
 //               more); splits add 4 and their sums' way through memory
 //   few rows    3 + the matrices once for every 16 tokens at 11 TB/s, a fifth more
 //               where an expert has several such tiles
@@ -679,9 +674,9 @@ static BlockShape block_shape(bool grad, bool direct, int64_t S, int64_t E, int6
     };
     const double bytes = (double)live * (double)M * (double)K, memory = bytes / 5.1e6;
     double least = 1e30;
-    const double step_us[3] = {0.46, 0.6, 0.95};
-    for (int i = 0; i < 3; ++i) {
-        const int64_t blocks = (outer + kTileRows - 1) / kTileRows * tiles(32 << i);
+    const double step_us[4] = {0.46, 0.6, 0.78, 0.95};
+    for (int i = 0; i < 4; ++i) {
+        const int64_t blocks = (outer + kTileRows - 1) / kTileRows * tiles(32 * (i + 1));
         const double step = bytes >= 64e6 && step_us[i] < 1.05 ? 1.05 : step_us[i];
         for (int64_t n = 1; n <= 16 && (n == 1 || steps / n >= 2); n *= 2) {
             const double rounds = (double)((blocks * n + 255) / 256), loop = rounds * (double)((steps + n - 1) / n) * step;
@@ -689,7 +684,7 @@ static BlockShape block_shape(bool grad, bool direct, int64_t S, int64_t E, int6
             if (n > 1) us += 4.0 + (double)(2 * n * S * outer) * sizeof(float) / 3.8e6;
             if (us < least) {
                 least = us;
-                best = {2 << i, n, 0};
+                best = {2 * (i + 1), n, 0};
             }
         }
     }
@@ -771,6 +766,7 @@ static hipError_t block_launch(const BlockArgs& a, void* ws, hipStream_t s) {
         else KM_GO2(NT, false);        \
     } while (0)
     if (shape.nt == 8) KM_GO(8);
+    else if (shape.nt == 6) KM_GO(6);
     else if (shape.nt == 4) KM_GO(4);
     else KM_GO(2);
 #undef KM_GO

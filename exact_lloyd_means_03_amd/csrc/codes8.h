@@ -7,6 +7,11 @@
 
 namespace km {
 
+template <int V>
+struct Int {
+    static constexpr int value = V;
+};
+
 constexpr int kBlock8 = 128;  // columns (of a matrix: and rows) that share a scale
 
 __host__ __device__ inline int64_t blocks8(int64_t n) { return (n + kBlock8 - 1) / kBlock8; }

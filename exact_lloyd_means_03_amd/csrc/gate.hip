@@ -59,6 +59,57 @@ __device__ __forceinline__ float gate_softmax(const float (&l)[EPL], float (&z)[
     return sum == 0.f ? 0.f : 1.f / sum;
 }
 
+// The `top` <= 16 largest of a row's keys at once.  The top-th largest of the lanes'
+// maxima bounds the choices from below; the few keys that reach it (a dozen of 256
+// where top is 8) are gathered, one a lane, and each lane counts the ones that come
+// before its own.  False where a row of the wave has more than 16 such keys (ties,
+// rows with few lanes left).  s: the group's 16 places.
+struct GatePick {
+    uint32_t key, e;  // the lane's (0: none)
+    int rank, total;  // its place, and the gathered ones
+};
+template <int N, typename F>
+__device__ __forceinline__ void each_rotation(F f) {  // f of the number of lanes turned: 1 .. 15
+    if constexpr (N < 16) {
+        f(Int<N>{});
+        each_rotation<N + 1>(f);
+    }
+}
+template <int EPL>
+__device__ __forceinline__ bool gate_pick(const uint32_t (&key)[EPL], int lane, int top, uint2* s, GatePick* p) {
+    uint32_t best = 0;
+#pragma unroll
+    for (int j = 0; j < EPL; ++j) best = best > key[j] ? best : key[j];
+    int c = 1;  // maxima that are not below the lane's
+    each_rotation<1>([&](auto n) { c += dpp<0x120 + decltype(n)::value>(best) >= best; });
+    const uint32_t bound = lane_max<16>(c >= top ? best : 0u), least = bound ? bound : 1u;
+    uint32_t n = 0;
+#pragma unroll
+    for (int j = 0; j < EPL; ++j) n += key[j] >= least;
+    uint32_t upto = n;  // with the lanes before
+    upto += dpp<0x111>(upto);
+    upto += dpp<0x112>(upto);
+    upto += dpp<0x114>(upto);
+    upto += dpp<0x118>(upto);
+    p->total = (int)lane_max<16>(upto);
+    if (__ballot(p->total > 16)) return false;
+    uint32_t at = upto - n;
+#pragma unroll
+    for (int j = 0; j < EPL; ++j)
+        if (key[j] >= least) s[at++] = uint2{key[j], (uint32_t)(j * 16 + lane)};
+    __builtin_amdgcn_wave_barrier();
+    const uint2 mine = s[lane];
+    p->key = lane < p->total ? mine.x : 0u;
+    p->e = mine.y;
+    p->rank = 0;
+    each_rotation<1>([&](auto n) {
+        const uint32_t k = dpp<0x120 + decltype(n)::value>(p->key), e = dpp<0x120 + decltype(n)::value>(p->e);
+        p->rank += (k > p->key) | ((k == p->key) & (e < p->e));
+    });
+    __builtin_amdgcn_wave_barrier();  // (read before the next row's are written)
+    return true;
+}
+
 // E sum_e shares[e] counts[e] / sum(counts) from dot = sum_e shares[e] counts[e]
 // (NaN shares make a NaN loss, also where no expert could be chosen).
 __device__ __forceinline__ float gate_loss(float dot, int64_t choices, int E) {
@@ -81,6 +132,8 @@ __global__ __launch_bounds__(gate_threads(L)) void k_gate(const T* __restrict__ 
                                                        int32_t* __restrict__ counts, float* __restrict__ shares,
                                                        float* __restrict__ loss) {
     constexpr int NT = gate_threads(L), G = NT / L, GW = 64 / L, W = NT / 64;
+    constexpr bool PICK = L == 16 && KR == 1;
+    __shared__ uint2 s_pick[PICK ? G : 1][16];
     extern __shared__ int32_t s_cnt[];  // [E + 1]; then float [W][E]
     const int tid = threadIdx.x, lane = tid & (L - 1), grp = tid / L;
     for (int j = tid; j <= E; j += NT) s_cnt[j] = 0;
@@ -106,6 +159,24 @@ __global__ __launch_bounds__(gate_threads(L)) void k_gate(const T* __restrict__ 
             rows += lane == 0;
 #pragma unroll
             for (int j = 0; j < EPL; ++j) acc[j] = fmaf(z[j], inv, acc[j]);
+        }
+        if constexpr (PICK) {
+            GatePick p;
+            if (gate_pick<EPL>(key, lane, top, s_pick[grp], &p)) {
+                const bool chosen = p.key && p.rank < top;
+                const float zk = chosen ? gate_exp(gate_value(p.key) - m) : 0.f;
+                const float sum = lane_sum<16>(zk), by = !normalize ? inv : sum == 0.f ? 0.f : 1.f / sum;
+                if (chosen) {
+                    atomicAdd(&s_cnt[p.e], 1);
+                    experts[t * top + p.rank] = (int32_t)p.e;
+                    weights[t * top + p.rank] = zk * by;
+                }
+                if (in && lane >= p.total && lane < top) {
+                    experts[t * top + lane] = -1;
+                    weights[t * top + lane] = 0.f;
+                }
+                continue;
+            }
         }
         uint32_t kk[KR], ke[KR];  // the choice k is lane k % L's: its key (0: none) and expert
 #pragma unroll
@@ -261,19 +332,23 @@ __global__ __launch_bounds__(kFoldExperts* kFoldParts) void k_gate_fold(
         }
         const float dot = lane_sum<64>((float)c * p);
         c = (int32_t)lane_fold<64>((uint32_t)c, [](uint32_t a, uint32_t b) { return a + b; });
+        int last = 0;
         if (tid == 0) {
             if (blockIdx.x == 0) counts[E] = n;
             __hip_atomic_store(&sums[blockIdx.x].dot, dot, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
             __hip_atomic_store(&sums[blockIdx.x].all, c, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-            if (__hip_atomic_fetch_add(ticket, 1, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT) == (int)gridDim.x - 1) {
-                float d = 0.f;
-                int64_t a = 0;
-                for (int i = 0; i < (int)gridDim.x; ++i) {
-                    d += __hip_atomic_load(&sums[i].dot, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-                    a += __hip_atomic_load(&sums[i].all, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-                }
-                loss[0] = gate_loss(d, a, E);
+            last = __hip_atomic_fetch_add(ticket, 1, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT) == (int)gridDim.x - 1;
+        }
+        if (__builtin_amdgcn_readfirstlane(last)) {
+            float d = 0.f;
+            int32_t a = 0;  // (choices: fewer than 2^31)
+            for (int i = tid; i < (int)gridDim.x; i += 64) {
+                d += __hip_atomic_load(&sums[i].dot, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+                a += __hip_atomic_load(&sums[i].all, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
             }
+            d = lane_sum<64>(d);
+            a = (int32_t)lane_fold<64>((uint32_t)a, [](uint32_t x, uint32_t y) { return x + y; });
+            if (tid == 0) loss[0] = gate_loss(d, a, E);
         }
     }
 }

@@ -110,6 +110,7 @@ SHAPES = [  # S, E, M, K, kind of offsets
     (200, 8, 8192, 256, "even"), (150, 1, 2048, 1024, "even"), (520, 2, 1024, 2048, "tail"), (1100, 1, 4096, 640, "even"),
     (2100, 1, 2048, 2048, "even"), (300, 1, 260, 4096, "even"), (130, 1, 4097, 257, "even"), (600, 1, 513, 2049, "even"),
     (40, 1, 700, 2050, "even"), (3000, 1, 1030, 1031, "even"), (9, 2, 15, 9, "even"), (70000, 2, 3, 5, "tail"),
+    (1530, 1, 4096, 400, "even"), (1530, 1, 4095, 401, "even"), (1530, 1, 400, 4096, "even"),
     (1, 1, 40, 40000, "even"), (1, 1, 40000, 40, "even"), (33000, 1, 16, 32, "even"),
 ]
 
