@@ -8,6 +8,8 @@ torch's autograd where an input requires a gradient, as in api.py.
 """
 from __future__ import annotations
 
+import functools
+
 import torch
 
 from . import _lib
@@ -43,9 +45,14 @@ def _output(t, name, dev, dtype, shape):
     return torch.empty_strided(shape, strides, dtype=dtype, device=dev)
 
 
+_entry = {}
+
+
 def _call(name, dev, *args):
     """The entry point on the current stream of dev, with dev current (kernels are launched on the current device)."""
-    fn = getattr(_lib._lib or _lib.load(), name)
+    fn = _entry.get(name)
+    if fn is None:
+        fn = _entry[name] = getattr(_lib.load(), name)
     if dev.index is None or dev.index == _current_device():
         st = fn(*args, _stream(dev))
     else:
@@ -55,10 +62,17 @@ def _call(name, dev, *args):
         _lib.check(st, name)
 
 
-def _workspace(ws, n, dev):
-    """The caller's workspace, or one of n bytes (None: none is needed)."""
+@functools.lru_cache(1024)
+def _bytes_of(query, *sizes):
+    """A workspace query of the library (sizes and types alone decide it)."""
+    return getattr(_lib.load(), query)(*sizes)
+
+
+def _workspace(ws, dev, query, *sizes):
+    """The caller's workspace, or one of the size asked for (None: none is needed)."""
     if ws is not None:
         return _tensor(ws, "workspace", dev, torch.uint8, None)
+    n = _bytes_of(query, *sizes)
     return torch.empty(n, dtype=torch.uint8, device=dev) if n else None
 
 
@@ -164,7 +178,7 @@ def kmeans_norm_grad(grad, h, weight=None, eps: float = 1e-6, grad_residual=None
         grad_weight = None
     else:
         grad_weight = _output(grad_weight, "grad_weight", dev, weight.dtype, (d,))
-        ws = _workspace(ws, 0 if ws is not None else _lib.load().kmeans_norm_grad_workspace_bytes(T, d, _DT[dt]), dev)
+        ws = _workspace(ws, dev, "kmeans_norm_grad_workspace_bytes", T, d, _DT[dt])
     _call("kmeans_norm_grad", dev, grad.data_ptr(), h.data_ptr(), _DT[dt], T, d, _ptr(grad_residual),
           *_weight_args(weight, dt), eps, grad_x.data_ptr(), _ptr(grad_weight), *_ws_args(ws))
     return grad_x, grad_weight
@@ -209,7 +223,7 @@ def kmeans_gate(logits, top: int, normalize: bool = True, experts=None, weights=
         counts = _output(counts, "counts", dev, torch.int32, (E + 1,))
         shares = _output(shares, "shares", dev, torch.float32, (E,))
         loss = _output(loss, "loss", dev, torch.float32, ())
-    ws = _workspace(ws, 0 if ws is not None else _lib.load().kmeans_gate_workspace_bytes(T, E), dev)
+    ws = _workspace(ws, dev, "kmeans_gate_workspace_bytes", T, E)
     _call("kmeans_gate", dev, logits.data_ptr(), _DT[logits.dtype], T, E, top, int(normalize), experts.data_ptr(),
           weights.data_ptr(), counts.data_ptr(), shares.data_ptr(), loss.data_ptr(), *_ws_args(ws))
     return experts, weights, counts, shares, loss
@@ -254,7 +268,7 @@ def kmeans_plan(experts, E: int, plan=None, ws=None):
     offsets = _output(offsets, "offsets", dev, torch.int32, (E + 1,))
     slots = _output(slots, "slots", dev, torch.int32, (T, top))
     order = _output(order, "order", dev, torch.int32, (T * top,))
-    ws = _workspace(ws, 0 if ws is not None else _lib.load().kmeans_plan_workspace_bytes(T, top, E), dev)
+    ws = _workspace(ws, dev, "kmeans_plan_workspace_bytes", T, top, E)
     _call("kmeans_plan", dev, experts.data_ptr(), T, top, E, offsets.data_ptr(), slots.data_ptr(), order.data_ptr(),
           *_ws_args(ws))
     return offsets, slots, order
@@ -351,7 +365,7 @@ def kmeans_block_product(x, x_scales, codes, scales, offsets=None, order=None, d
         return _BlockProduct.apply(x, codes, scales, offsets, order, dtype)
     x, x_scales = _rows8(x, x_scales, "x", K)
     out = _output(out, "out", dev, dtype, (S, M))
-    ws = _workspace(ws, 0 if ws is not None else _lib.load().kmeans_block_product_workspace_bytes(S, E, M, K), dev)
+    ws = _workspace(ws, dev, "kmeans_block_product_workspace_bytes", S, E, M, K)
     _call("kmeans_block_product", dev, x.data_ptr(), x_scales.data_ptr(), S, codes.data_ptr(), scales.data_ptr(), E, M, K,
           _ptr(offsets), _ptr(order), top, out.data_ptr(), _DT[dtype], *_ws_args(ws))
     return out
@@ -373,7 +387,7 @@ def kmeans_block_product_grad(grad, grad_scales, codes, scales, offsets=None, dt
         _no_gradient("kmeans_block_product_grad", grad=grad, grad_scales=grad_scales, codes=codes, scales=scales)
     grad, grad_scales = _rows8(grad, grad_scales, "grad", M)
     out = _output(out, "out", dev, dtype, (S, K))
-    ws = _workspace(ws, 0 if ws is not None else _lib.load().kmeans_block_product_grad_workspace_bytes(S, E, M, K), dev)
+    ws = _workspace(ws, dev, "kmeans_block_product_grad_workspace_bytes", S, E, M, K)
     _call("kmeans_block_product_grad", dev, grad.data_ptr(), grad_scales.data_ptr(), S, codes.data_ptr(),
           scales.data_ptr(), E, M, K, _ptr(offsets), out.data_ptr(), _DT[dtype], *_ws_args(ws))
     return out
