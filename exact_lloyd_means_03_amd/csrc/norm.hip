@@ -224,7 +224,8 @@ __global__ __launch_bounds__(64 * WPR) void k_norm_grad(const T* __restrict__ gr
 #pragma unroll
             for (int i = 0; i < WPR; ++i) hh += s[2 * i], uh += s[2 * i + 1];
         }
-        const float r = 1.f / sqrtf(hh / dd + eps), k = r * r * r * (uh / dd);
+        // (r^3 by itself leaves float32 where h is beyond 2^42 or, with eps 0, below 2^-42)
+        const float r = 1.f / sqrtf(hh / dd + eps), k = uh / dd * r * r * r;
 #pragma unroll
         for (int i = 0; i < NC; ++i) {
             const int c = c0 + 64 * WPR * i, e0 = chunk_at<T>(c, d);

@@ -224,6 +224,17 @@ def test_long_rows(km, dtype, T, d):
     _check_codes(q, s, hd * r * w.double(), 96 * U32, "codes")
 
 
+@pytest.mark.parametrize("size", [2.0 ** -50, 2.0 ** 50])
+def test_grad_of_large_and_small_rows(km, size):
+    # grad_x falls as the rows grow: h = size * v has 1 / size times v's (powers of two: the
+    # same bits), also where r^3 is out of float32's range
+    g, v = _rows((5, 300), torch.float32, 41, 0.3), _rows((5, 300), torch.float32, 42)
+    weight = 1.0 + 0.2 * _rows((300,), torch.float32, 43)
+    one, gw1 = km.kmeans_norm_grad(g, v, weight, 0.0)
+    gx, gw = km.kmeans_norm_grad(g, v * size, weight, 0.0)
+    assert torch.equal(gx * size, one) and torch.equal(gw, gw1)
+
+
 def test_grad_by_differences(km):
     # along a direction v: (f(h + e v) - f(h - e v)) / 2 e of f = <g, y>, in float32 sums of
     # 40 x 160 terms of size 1 (off by 6400 u32 / 2 e = 0.02 at e = 1/100) and a third-order
