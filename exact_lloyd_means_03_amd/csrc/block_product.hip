@@ -35,23 +35,8 @@ __device__ __forceinline__ u32x4 move_down(u32x4 t, int by) {
     return v;
 }
 
-// 16 codes of a row of `len` at p, of which p[i], i < n, are in the row (n may be
-// negative): the others as zeros.
-__device__ __forceinline__ u32x4 load16_end(const uint8_t* __restrict__ p, int n, int64_t len) {
-    if (n >= 16) return *(const u32x4_byte*)p;
-    u32x4 v{0, 0, 0, 0};
-    if (n <= 0) return v;
-    if (len >= 16) return move_down(*(const u32x4_byte*)(p + n - 16), 16 - n);  // the row's last 16
-#pragma nounroll
-    for (int i = 0; i < n; ++i) {
-        const uint32_t c = (uint32_t)p[i] << (8 * (i & 3));
-#pragma unroll
-        for (int j = 0; j < 4; ++j) v[j] |= i >> 2 == j ? c : 0u;
-    }
-    return v;
-}
-
-// The same without branches, of a row that has 16 codes at least.
+// 16 codes of a row of 16 at least at p, of which p[i], i < n, are in the row (n may
+// be negative): the others as zeros, without branches.
 __device__ __forceinline__ u32x4 load16_in(const uint8_t* __restrict__ p, int n) {
     const int by = n >= 16 ? 0 : 16 - n;
     return move_down(*(const u32x4_byte*)(p - by), by < 16 ? by : 16);
@@ -81,80 +66,46 @@ __device__ __forceinline__ int64_t source_row(const int32_t* __restrict__ order,
     return o >= 0 && o < S ? o / (int32_t)top : -1;
 }
 
-// Any rows: few unaligned ones, and matrices too small for the other kernels.  out =
-// W x^T on 16 x 16 x 128 instructions, the matrix as A: a block takes 16 rows of the
-// matrix and 16 NT tokens, its WK waves every WK-th block of 128 columns, whose sums
-// are added in LDS in order.  Codes go from memory to operands; GRAD reads the
-// columns of the matrix byte by byte.  One row by 4096 x 4096: 6.8 us; 64 rows over
-// 16 experts of 4096 x 2048: 33 us, an access a lane in the texture path.
-template <typename O, int WK, int NT, bool GRAD>
-__global__ __launch_bounds__(64 * WK) void k_block_few(const uint8_t* __restrict__ x, const float* __restrict__ xs,
-                                                       int64_t S, const uint8_t* __restrict__ codes,
-                                                       const float* __restrict__ scales, int E, int64_t M, int64_t K,
-                                                       const int32_t* __restrict__ offsets,
-                                                       const int32_t* __restrict__ order, int64_t top,
-                                                       int64_t y0, O* __restrict__ out) {
-    constexpr int TT = 16 * NT;
-    __shared__ f32x4 s_sum[WK][NT][64];
-    const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int r = lane & 15, q = lane >> 4;
-    const Segment g = find_segment(offsets, S, E, TT, (int)(y0 + blockIdx.y));
+// Inner lengths below 16 codes, too short for the other kernels' copies of 16 bytes:
+// out = W x^T, one 16 x 16 x 128 instruction for 16 rows of the matrix (as A; GRAD:
+// its columns) and 16 tokens, a wave each.  The lanes of the first 16 codes read them
+// byte by byte; the others hold zeros.
+template <typename O, bool GRAD>
+__global__ __launch_bounds__(64) void k_block_short(const uint8_t* __restrict__ x, const float* __restrict__ xs, int64_t S,
+                                                    const uint8_t* __restrict__ codes, const float* __restrict__ scales,
+                                                    int E, int64_t M, int64_t K, const int32_t* __restrict__ offsets,
+                                                    const int32_t* __restrict__ order, int64_t top, int64_t y0,
+                                                    O* __restrict__ out) {
+    const int lane = threadIdx.x, r = lane & 15, q = lane >> 4;
+    const Segment g = find_segment(offsets, S, E, 16, (int)(y0 + blockIdx.y));
     if (g.e < 0) return;
-    // inner: the length summed over; outer: the results of a row
-    const int64_t inner = GRAD ? M : K, outer = GRAD ? K : M, ib = blocks8(inner), kb = blocks8(K);
-    const int64_t o0 = (int64_t)blockIdx.x * 16, ob = o0 / kBlock8;
-    f32x4 acc[NT];
-#pragma unroll
-    for (int n = 0; n < NT; ++n) acc[n] = f32x4{0.f, 0.f, 0.f, 0.f};
+    const int64_t outer = GRAD ? K : M, o0 = (int64_t)blockIdx.x * 16;
+    const int inner = (int)(GRAD ? M : K);
+    f32x4 v{0.f, 0.f, 0.f, 0.f};
     if (g.e < E) {
-        const uint8_t* wm = codes + (int64_t)g.e * M * K;
-        const float* ws = scales + (int64_t)g.e * blocks8(M) * kb;
+        const int64_t src = source_row(order, top, S, g.p0 + (r < g.n ? r : g.n - 1));
         const int64_t o = o0 + r < outer ? o0 + r : outer - 1;
-        int64_t src[NT];
+        const uint8_t* wp = codes + (int64_t)g.e * M * K + (GRAD ? o : o * K);
+        const uint8_t* xp = x + (src < 0 ? 0 : src) * inner;
+        const int64_t step = GRAD ? K : 1;
+        u32x4 a{0, 0, 0, 0}, b{0, 0, 0, 0};
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
-            src[n] = source_row(order, top, S, g.p0 + (n * 16 + r < g.n ? n * 16 + r : g.n - 1));
-        for (int64_t b = w; b < ib; b += WK) {
-            const int64_t i0 = b * kBlock8 + q * 32;
-            const int left = (int)(inner - i0 < 32 ? inner - i0 : 32);  // (negative: none)
-            u32x4 a[2];
-            if constexpr (GRAD) {
-                uint32_t v[8];
-#pragma unroll
-                for (int j = 0; j < 8; ++j) v[j] = 0;
-#pragma unroll
-                for (int j = 0; j < 32; ++j)
-                    if (j < left) v[j / 4] |= (uint32_t)wm[(i0 + j) * K + o] << (8 * (j % 4));
-                a[0] = u32x4{v[0], v[1], v[2], v[3]};
-                a[1] = u32x4{v[4], v[5], v[6], v[7]};
-            } else {
-                a[0] = load16_end(wm + o * K + i0, left, K);
-                a[1] = load16_end(wm + o * K + i0 + 16, left - 16, K);
+        for (int j = 0; j < 15; ++j)
+            if (q == 0 && j < inner) {
+                a[j / 4] |= (uint32_t)wp[j * step] << (8 * (j % 4));
+                b[j / 4] |= (uint32_t)xp[j] << (8 * (j % 4));
             }
-            const float sw = GRAD ? ws[b * kb + ob] : ws[ob * kb + b];
+        // (one block of the inner length)
+        const float s = scales[(int64_t)g.e * blocks8(outer) + o0 / kBlock8] * xs[src < 0 ? 0 : src];
+        const u32x4 no{0, 0, 0, 0};
+        const f32x4 d = mfma8(join8(a, no), join8(b, no), f32x4{0.f, 0.f, 0.f, 0.f});
+        if (src >= 0) {  // (codes and scales that are no numbers stay out of a row of none)
 #pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                const uint8_t* p = x + src[n] * inner + i0;
-                const int have = src[n] < 0 ? 0 : left;
-                const u32x4 x0 = load16_end(p, have, inner), x1 = load16_end(p + 16, have - 16, inner);
-                const float s = sw * (src[n] < 0 ? 0.f : xs[src[n] * ib + b]);
-                const f32x4 d = mfma8(join8(a[0], a[1]), join8(x0, x1), f32x4{0.f, 0.f, 0.f, 0.f});
-#pragma unroll
-                for (int i = 0; i < 4; ++i) acc[n][i] = fmaf(s, d[i], acc[n][i]);
-            }
+            for (int i = 0; i < 4; ++i) v[i] = s * d[i];
         }
     }
-#pragma unroll
-    for (int n = 0; n < NT; ++n) s_sum[w][n][lane] = acc[n];
-    __syncthreads();
-    for (int i = threadIdx.x; i < NT * 64; i += 64 * WK) {
-        const int n = i >> 6, l = i & 63, tk = n * 16 + (l & 15);
-        f32x4 v = s_sum[0][n][l];
-#pragma unroll
-        for (int o = 1; o < WK; ++o) v += s_sum[o][n][l];
-        const int64_t o = o0 + (l >> 4) * 4;
-        if (tk < g.n && o < outer) store_results<O>(out + (g.p0 + tk) * outer + o, outer - o, v);
-    }
+    const int64_t o = o0 + q * 4;
+    if (r < g.n && o < outer) store_results<O>(out + (g.p0 + r) * outer + o, outer - o, v);
 }
 
 // Many rows.  The same product on blocks of 256 rows of the matrix (GRAD: its
@@ -663,8 +614,8 @@ struct BlockShape {
 static BlockShape block_shape(bool grad, bool direct, int64_t S, int64_t E, int64_t M, int64_t K) {
     const int64_t inner = grad ? M : K, outer = grad ? K : M, steps = blocks8(inner);
     BlockShape best{0, 1, 0};
-    // (the copies of unaligned rows through registers take 16 codes of a row, or of a matrix, at least)
-    if (!direct && (inner < 16 || M * K < 16)) return best;
+    // (the copies of unaligned rows through registers take 16 codes of a row at least)
+    if (inner < 16) return best;
     const int64_t live = S < E ? S : E;
     if (live < 1) return best;
     // an expert's last tile is half full on average
@@ -740,8 +691,8 @@ static hipError_t block_launch(const BlockArgs& a, void* ws, hipStream_t s) {
         // (the grid's second axis holds 65535 token tiles)
         const int64_t all = segment_tiles(a.S, a.E, a.offsets, 16), most = 1 << 15;
         for (int64_t y0 = 0; y0 < all; y0 += most)
-            hipLaunchKernelGGL((k_block_few<O, 8, 1, GRAD>),
-                               dim3((unsigned)((outer + 15) / 16), (unsigned)(all - y0 < most ? all - y0 : most)), dim3(512), 0,
+            hipLaunchKernelGGL((k_block_short<O, GRAD>),
+                               dim3((unsigned)((outer + 15) / 16), (unsigned)(all - y0 < most ? all - y0 : most)), dim3(64), 0,
                                s, (const uint8_t*)a.x, a.x_scales, a.S, (const uint8_t*)a.codes, a.scales, (int)a.E, a.M,
                                a.K, a.offsets, a.order, a.top, y0, (O*)a.out);
         return hipGetLastError();

@@ -283,6 +283,22 @@ def test_special_codes(km):
     assert torch.equal(y.isnan(), bad)
 
 
+@pytest.mark.parametrize("S,M,K", [(20, 40, 9), (20, 40, 200), (20, 48, 256), (600, 256, 256), (600, 256, 200)])
+def test_rows_of_none_among_others(km, S, M, K):
+    # an order of -1 is a row of zeros, also where the matrix holds a NaN code and an infinite
+    # scale; K below 16, unaligned, aligned rows, few and many
+    x, xs, w, ws = _codes((S, K), 1), _scales((S, -(-K // 128)), 2), _codes((M, K), 3), _scales((-(-M // 128), -(-K // 128)), 4)
+    order = torch.arange(S - 1, -1, -1, dtype=torch.int32, device="cuda")
+    order[::3] = -1
+    want = km.kmeans_block_product(x[order.clamp(min=0).long()].contiguous(), xs[order.clamp(min=0).long()].contiguous(), w, ws)
+    want[::3] = 0
+    assert torch.equal(km.kmeans_block_product(x, xs, w, ws, order=order), want)
+    w.view(torch.uint8)[5, K - 1] = 0x7f
+    ws[-1, 0] = float("inf")
+    y = km.kmeans_block_product(x, xs, w, ws, order=order)
+    assert (y[::3] == 0).all() and y[1::3, 5].isnan().all()
+
+
 def test_refusals(km):
     x, xs = _codes((4, 256), 1), _scales((4, 2), 2)
     w, ws = _codes((2, 128, 256), 3), _scales((2, 1, 2), 4)
