@@ -461,6 +461,8 @@ class _BlockProduct(torch.autograd.Function):
         if order is not None:
             # the rows back at the tokens that they were gathered from
             S = order.numel()
+            if S == 0:
+                return rows.new_zeros((ctx.T, rows.shape[1])), None, None, None, None, None
             slots = torch.full((S + 1,), -1, dtype=torch.int32, device=order.device)
             slots[torch.where((order >= 0) & (order < S), order, S).long()] = torch.arange(
                 S, dtype=torch.int32, device=order.device)

@@ -299,6 +299,16 @@ def test_rows_of_none_among_others(km, S, M, K):
     assert (y[::3] == 0).all() and y[1::3, 5].isnan().all()
 
 
+@pytest.mark.parametrize("T,top", [(0, 2), (4, 0)])
+def test_autograd_without_choices(km, T, top):
+    x = torch.zeros((T, 256), device="cuda").requires_grad_()
+    order = torch.empty(T * top, dtype=torch.int32, device="cuda")
+    y = km.kmeans_block_product(x, None, _codes((128, 256), 1), _scales((1, 2), 2), order=order)
+    assert y.shape == (0, 128)
+    y.sum().backward()
+    assert x.grad.shape == x.shape and (x.grad == 0).all()
+
+
 def test_refusals(km):
     x, xs = _codes((4, 256), 1), _scales((4, 2), 2)
     w, ws = _codes((2, 128, 256), 3), _scales((2, 1, 2), 4)
