@@ -165,3 +165,34 @@ def test_rows_before_and_behind_stay(km):
     assert torch.equal(big[20:120], rows) and (big[:20] == 3).all() and (big[120:] == 3).all()
     held = torch.cat([q.view(torch.uint8), torch.full((7, 256), 0x7f, dtype=torch.uint8, device="cuda")]).view(torch.float8_e4m3fn)
     assert torch.equal(km.kmeans_block_product(held[:50], s, layer.codes, layer.scales, offsets, order=order), rows)
+
+
+def test_trained_in_a_graph(km):
+    # forward and backward recorded by autograd inside one captured graph, the rows gathered
+    layer = Layer(km, 256, 6, 2, 11)
+    x, residual, gy = layer.tokens(150, 12)
+    x.requires_grad_()
+
+    def step():
+        y, h = km.kmeans_norm(x, layer.weight, residual=residual)
+        experts, weights, _, _, loss = km.kmeans_gate(y @ layer.router, layer.top)
+        offsets, slots, order = km.kmeans_plan(experts, layer.E)
+        rows = km.kmeans_block_product(y, None, layer.codes, layer.scales, offsets, order=order)
+        out = km.kmeans_combine(rows, slots, weights)
+        return torch.autograd.grad((out, loss), x, (gy, torch.ones_like(loss)))[0]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        grad = step()
+    for seed in range(4):
+        with torch.no_grad():
+            for a, b in zip((x, residual, gy), layer.tokens(150, 20 + seed)):
+                a.copy_(b)
+        grad.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(grad, step()), seed
