@@ -1,5 +1,6 @@
 // Products of 8-bit rows with 8-bit matrices that have a float32 scale for each
 // block of 128 x 128, one matrix per expert, and the gradient of their input.
+#include "block_copy.h"
 #include "codes.h"
 #include "codes8.h"
 
@@ -38,7 +39,7 @@ __device__ __forceinline__ u32x4 move_down(u32x4 t, int by) {
 // 16 codes of a row of 16 at least at p, of which p[i], i < n, are in the row (n may
 // be negative): the others as zeros, without branches.
 __device__ __forceinline__ u32x4 load16_in(const uint8_t* __restrict__ p, int n) {
-    const int by = n >= 16 ? 0 : 16 - n;
+    const int by = tile_back(n);
     return move_down(*(const u32x4_byte*)(p - by), by < 16 ? by : 16);
 }
 
@@ -128,8 +129,6 @@ __global__ __launch_bounds__(64) void k_block_short(const uint8_t* __restrict__ 
 // are copied through registers.
 constexpr int kTileThreads = 256, kTileRows = 256;
 
-constexpr int kTileStages = 3;
-
 template <int NT>
 struct BlockTile {
     static constexpr int TT = 16 * NT;
@@ -141,10 +140,6 @@ struct BlockTile {
     static constexpr int BYTES = SRC + TT * 4;
     static constexpr int LOADS = NT / 2 + 8 + 2;             // a wave's direct loads of a step
 };
-
-// 16-byte chunk of row m (of 64 columns) that holds columns 16 c .. 16 c + 15: the
-// 32 rows that a transposing read touches spread over all banks.
-__device__ __forceinline__ int tile_chunk(int c, int m) { return c ^ ((m >> 2 & 1) ^ (m >> 4 & 3)); }
 
 // What direct loads of codes behind a row's end read.
 __device__ const u32x4 g_no_codes = {0, 0, 0, 0};
@@ -207,19 +202,11 @@ __global__ __launch_bounds__(kTileThreads, 1) void k_block_tile(
         uint32_t wo[NW];
         const int wrow = GRAD ? lane >> 2 : lane >> 3;
 #pragma unroll
-        for (int i = 0; i < NW; ++i) {
-            if constexpr (GRAD) {
-                const int64_t col = o0 + tile_chunk(lane & 3, i * 16 + wrow) * 16;
-                wo[i] = (uint32_t)((i * 16 + wrow) * K) + (uint32_t)(col < outer ? col : 0);
-            } else {
-                const int64_t left = outer - 1 - o0, row = i * 8 + wrow;
-                wo[i] = (uint32_t)((row < left ? row : left < 0 ? 0 : left) * K) + ((lane & 7) ^ (lane >> 3)) * 16;
-            }
-        }
+        for (int i = 0; i < NW; ++i) wo[i] = tile_matrix_at(GRAD, K, outer, o0, i, lane);
         auto wbase = [&](int64_t st) { return wb + st * kBlock8 * (GRAD ? K : 1); };
         auto to_x = [&](int stage, int i) { return s_mem + stage * L::STAGE + (i * kTileThreads + w * 64) * 16; };
         auto to_w = [&](int stage, int i) { return s_mem + stage * L::STAGE + L::X + w * (64 * kBlock8) + i * 1024; };
-        // direct load i of step st; LAST: of a step that the inner length ends in
+        // direct load i of step st; LAST: of a step that may need bounds
         auto load = [&](int64_t st, int stage, int i, auto last_tag) {
             constexpr bool LAST = decltype(last_tag)::value;
             const int left = (int)(inner - st * kBlock8);
@@ -380,9 +367,9 @@ __global__ __launch_bounds__(kTileThreads, 1) void k_block_tile(
         landed(Int<ST - 1>{});
 #pragma unroll
         for (int k = 0; k < PARTS; ++k) read(0, f[0], k);
-        // steps during which no loads of the last one begin, then the others
+        // steps during which only loads without bounds begin, then the others
         int64_t st = s0;
-        for (; st + 1 + ST < s1 - 1; st += 2) {
+        for (; st + 1 + ST < tile_free_end(s1, GRAD, DIRECT); st += 2) {
             step(st, Int<0>{}, Int<0>{});
             step(st + 1, Int<1>{}, Int<0>{});
         }
