@@ -210,19 +210,13 @@ def kmeans_gate(logits, top: int, normalize: bool = True, experts=None, weights=
     if _grads(logits):
         _no_buffers("kmeans_gate", experts, weights, counts, shares, loss)
         return _Gate.apply(logits, top, normalize, ws)
-    n = T * top
-    if n and top > 0 and experts is weights is counts is shares is loss is None:
-        # five small outputs in one allocation
-        experts, weights, counts, shares, loss = torch.unsafe_split_with_sizes(
-            torch.empty_strided((2 * n + 2 * E + 2,), (1,), dtype=torch.float32, device=dev), (n, n, E + 1, E, 1))
-        experts, weights = experts.view(torch.int32).view(T, top), weights.view(T, top)
-        counts, loss = counts.view(torch.int32), loss.view(())
-    else:
-        experts = _output(experts, "experts", dev, torch.int32, (T, top))
-        weights = _output(weights, "weights", dev, torch.float32, (T, top))
-        counts = _output(counts, "counts", dev, torch.int32, (E + 1,))
-        shares = _output(shares, "shares", dev, torch.float32, (E,))
-        loss = _output(loss, "loss", dev, torch.float32, ())
+    # (each a tensor of its own: parts of one allocation would be views, which autograd does
+    # not let a caller scale in place, and a loss that is kept would keep the choices)
+    experts = _output(experts, "experts", dev, torch.int32, (T, top))
+    weights = _output(weights, "weights", dev, torch.float32, (T, top))
+    counts = _output(counts, "counts", dev, torch.int32, (E + 1,))
+    shares = _output(shares, "shares", dev, torch.float32, (E,))
+    loss = _output(loss, "loss", dev, torch.float32, ())
     ws = _workspace(ws, dev, "kmeans_gate_workspace_bytes", T, E)
     _call("kmeans_gate", dev, logits.data_ptr(), _DT[logits.dtype], T, E, top, int(normalize), experts.data_ptr(),
           weights.data_ptr(), counts.data_ptr(), shares.data_ptr(), loss.data_ptr(), *_ws_args(ws))
