@@ -356,7 +356,7 @@ def kmeans_block_product(x, x_scales, codes, scales, offsets=None, order=None, d
             _no_gradient("kmeans_block_product", x=x, x_scales=x_scales)
         _no_gradient("kmeans_block_product", x_scales=x_scales, codes=codes, scales=scales)
         _no_buffers("kmeans_block_product", out)
-        return _BlockProduct.apply(x, codes, scales, offsets, order, dtype)
+        return _BlockProduct.apply(x, x_scales, codes, scales, offsets, order, dtype, ws)
     x, x_scales = _rows8(x, x_scales, "x", K)
     out = _output(out, "out", dev, dtype, (S, M))
     ws = _workspace(ws, dev, "kmeans_block_product_workspace_bytes", S, E, M, K)
@@ -442,10 +442,10 @@ class _Gate(torch.autograd.Function):
 
 class _BlockProduct(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, x, codes, scales, offsets, order, dtype):
+    def forward(ctx, x, x_scales, codes, scales, offsets, order, dtype, ws):
         ctx.T, ctx.dtype = x.shape[0], x.dtype
         ctx.save_for_backward(codes, scales, offsets, order)
-        return kmeans_block_product(x, None, codes, scales, offsets, order, dtype)
+        return kmeans_block_product(x, x_scales, codes, scales, offsets, order, dtype, ws=ws)
 
     @staticmethod
     @torch.autograd.function.once_differentiable
@@ -456,9 +456,9 @@ class _BlockProduct(torch.autograd.Function):
             # the rows back at the tokens that they were gathered from
             S = order.numel()
             if S == 0:
-                return rows.new_zeros((ctx.T, rows.shape[1])), None, None, None, None, None
+                return rows.new_zeros((ctx.T, rows.shape[1])), *[None] * 7
             slots = torch.full((S + 1,), -1, dtype=torch.int32, device=order.device)
             slots[torch.where((order >= 0) & (order < S), order, S).long()] = torch.arange(
                 S, dtype=torch.int32, device=order.device)
             rows = kmeans_combine(rows, slots[:S].view(ctx.T, -1))
-        return rows, None, None, None, None, None
+        return rows, *[None] * 7
