@@ -10,6 +10,7 @@ from __future__ import annotations
 import ctypes
 
 import torch
+import torch.autograd.forward_ad as _forward
 
 from . import _lib
 
@@ -387,6 +388,25 @@ def _output(t, name, dev, dtype, shape):
     return torch.empty(shape, dtype=dtype, device=dev) if t is None else _tensor(t, name, dev, dtype, shape)
 
 
+def _grads(*tensors):
+    """Whether autograd records a call of these inputs (None among them).  Forward-mode
+    tangents, which no operator takes along, are refused."""
+    if getattr(_forward, "_current_level", 0) >= 0:  # (dual tensors live inside a dual_level)
+        _no_tangents(tensors)
+    for t in tensors:
+        if t is not None and t.requires_grad:
+            return torch.is_grad_enabled()
+    return False
+
+
+def _no_tangents(tensors):
+    # (a dual tensor does not require a gradient, and results would pass for constants)
+    for t in tensors:
+        if t is not None and _forward.unpack_dual(t).tangent is not None:
+            raise ValueError("the operators have no forward-mode derivatives: pass the primal of a dual tensor "
+                             "(torch.autograd.forward_ad.unpack_dual)")
+
+
 def _no_gradient(name, **tensors):
     # a result without history would lose these tensors' gradients without a word
     for arg, t in tensors.items():
@@ -416,7 +436,7 @@ def kmeans_lookup(table, labels, scale: float = 1.0, out=None):
     _tensor(labels, "labels", dev, torch.int32, None)
     if labels.dim() != 2 or labels.shape[0] != B:
         raise ValueError("labels must be [B, N] int32")
-    if table.requires_grad and torch.is_grad_enabled():
+    if _grads(table):
         _no_buffers("kmeans_lookup", out)
         return _Lookup.apply(table, labels, scale)
     N = labels.shape[1]
@@ -440,7 +460,7 @@ def kmeans_lookup_grad(grad, labels, V: int, scale: float = 1.0, out=None, ws=No
     _tensor(grad, "grad", None, None, None)
     if grad.dim() != 3:
         raise ValueError("grad must be [B, N, d]")
-    if grad.requires_grad:
+    if _grads(grad):
         _no_gradient("kmeans_lookup_grad", grad=grad)
     B, N, d = grad.shape
     dev = grad.device
@@ -479,7 +499,7 @@ def kmeans_dispatch(x, experts, E: int, rows=None, plan=None, ws=None):
     _tensor(experts, "experts", dev, torch.int32, None)
     if experts.dim() != 2 or experts.shape[0] != T:
         raise ValueError("experts must be [T, top] int32")
-    if x.requires_grad and torch.is_grad_enabled():
+    if _grads(x):
         _no_buffers("kmeans_dispatch", rows, plan)
         return _Dispatch.apply(x, experts, E, ws)
     top = experts.shape[1]
@@ -516,7 +536,7 @@ def kmeans_combine(rows, slots, weights=None, out=None):
     T, top, d, dev = _sorted_rows(rows, slots)
     if weights is not None:
         _tensor(weights, "weights", dev, torch.float32, (T, top))
-    if (rows.requires_grad or weights is not None and weights.requires_grad) and torch.is_grad_enabled():
+    if _grads(rows, weights):
         _no_buffers("kmeans_combine", out)
         return _Combine.apply(rows, slots, weights)
     out = _output(out, "out", dev, rows.dtype, (T, d))
@@ -535,7 +555,7 @@ def kmeans_combine_grad(grad, rows, slots, order, weights, grad_rows=None, grad_
     _tensor(grad, "grad", dev, rows.dtype, (T, d))
     _tensor(order, "order", dev, torch.int32, (T * top,))
     _tensor(weights, "weights", dev, torch.float32, (T, top))
-    if grad.requires_grad or rows.requires_grad or weights.requires_grad:
+    if _grads(grad, rows, weights):
         _no_gradient("kmeans_combine_grad", grad=grad, rows=rows, weights=weights)
     grad_rows = _output(grad_rows, "grad_rows", dev, rows.dtype, (T * top, d))
     grad_weights = _output(grad_weights, "grad_weights", dev, torch.float32, (T, top))
@@ -596,11 +616,11 @@ def _codes_call(name, x, codes, table, M, K, scales, group, offsets, out, n_out,
         _tensor(offsets, "offsets", dev, torch.int32, (E + 1,))
     elif E != 1:
         raise ValueError("offsets are needed for more than one expert")
-    if x.requires_grad or table.requires_grad or (scales is not None and scales.requires_grad):
+    if _grads(x, table, scales):
         _no_gradient(name, table=table, scales=scales)
         if name == "kmeans_codes_product_grad":
             _no_gradient(name, grad=x)
-        elif x.requires_grad and torch.is_grad_enabled():
+        else:
             _no_buffers(name, out)
             return _Product.apply(x, codes, table, M, scales, group, offsets)
     out = _output(out, "out", dev, dt, (S, n_out))

@@ -13,7 +13,7 @@ import functools
 import torch
 
 from . import _lib
-from .api import _DT, _bytes, _no_buffers, _no_gradient, _ptr, _stream, _tensor, kmeans_combine
+from .api import _DT, _bytes, _grads, _no_buffers, _no_gradient, _ptr, _stream, _tensor, kmeans_combine
 
 E4M3 = torch.float8_e4m3fn
 BLOCK = 128
@@ -21,14 +21,6 @@ BLOCK = 128
 
 def _blocks(n):
     return -(-n // BLOCK)
-
-
-def _grads(*tensors):
-    """Whether autograd records a call of these inputs (None among them)."""
-    for t in tensors:
-        if t is not None and t.requires_grad:
-            return torch.is_grad_enabled()
-    return False
 
 
 _current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
@@ -92,7 +84,7 @@ def kmeans_quantize(x, rows: int = 1, codes=None, scales=None):
         raise ValueError("x must be [M, K] or [B, M, K]")
     if rows not in (1, BLOCK):
         raise ValueError("rows must be 1 or 128")
-    if x.requires_grad:
+    if _grads(x):
         _no_gradient("kmeans_quantize", x=x)
     dev, shape = x.device, tuple(x.shape)
     M, K = shape[-2:]
