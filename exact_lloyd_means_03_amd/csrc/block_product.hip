@@ -121,9 +121,10 @@ __global__ __launch_bounds__(64) void k_block_short(const uint8_t* __restrict__ 
 // 64 columns and reads them transposed (ds_read_b64_tr_b8: a lane receives one
 // column of eight rows).
 //
-// A wave runs alone on its SIMD, so nothing else hides its latencies: between the matrix instructions of a step stand the reads of the next
-// step's operands from LDS, the direct loads of a later one, and the scaling of
-// the results of two instructions before.
+// A wave runs alone on its SIMD, so nothing else hides its latencies: between the
+// matrix instructions of a step stand the reads of the next step's operands from
+// LDS, the direct loads of a later one, and the scaling of the results of two
+// instructions before.
 //
 // DIRECT: rows of x and of the matrix start at 16-byte boundaries; otherwise codes
 // are copied through registers.
@@ -576,23 +577,35 @@ __global__ __launch_bounds__(256) void k_block_join(const float* __restrict__ pa
 //   few rows    3 + the matrices once for every 16 tokens at 11 TB/s, a fifth more
 //               where an expert has several such tiles
 //   both        no less than the matrices take from memory, 5.1 TB/s
-// Measured (bf16; 17: four waves a group, 18: two, 24: one; nt / splits; the last
-// column: the rule's choice), us a call in a graph:
-//   rows, matrices        17     18     24    2/1    2/2    2/4    4/1    4/2    8/1    8/2   rule
-//      1, 4096 x 4096    7.5   10.3   16.1   17.9          10.8   20.9                      10: 6.4
-//     64, 4096 x 4096   10.9   11.5   17.7   18.9          13.6   23.7                       17
-//    256, 4096 x 4096   32.7   27.2   23.9   19.0   20.3   22.9   23.3   22.0   33.9   28.6  2/1
-//   1024, 4096 x 4096  116.0   97.1   85.3   39.6   53.5   76.5   27.4   42.9   35.0   35.4  4/1
-//   4096, 4096 x 4096  463.7  364.6  323.0  141.2  202.8  325.5  100.4  154.3   83.3  128.5  8/1
-//     64, 16 4096 x 2048 29.6  27.4   25.5   29.2          43.2   29.3                       24
-//    128, 8 4096 x 4096 37.8   36.8   39.5   38.2   32.5   46.0   38.7   32.6   40.5   34.5  2/2
-//    512, 8 of those    77.6   69.4   69.6   57.5   58.5   66.9   43.9   49.6   47.3   39.7  8/2
-//   4096, 8 of those   487.3  398.2  361.9  200.4  270.4  366.9  141.6  198.8  120.5  160.0  8/1
+// Where the matrices come from memory, tiles of 64, 96 and 128 tokens tie in the model
+// as long as their rounds do, and the smallest is taken.  Measured (bf16, us a call in
+// a graph that repeats it, so that matrices of up to 256 MB are in the memory-side
+// cache; s8 .. s1: the kernel of few rows with 8 .. 1 waves a group; token tiles /
+// splits; last what this function chooses):
+//   rows, matrices                s8     s4     s2     s1    2/1    2/2    4/1    4/2    6/1    8/1    8/2  rule
+//       1, 4096 x 4096           5.2    6.4    8.6   13.4   17.4   12.5   20.2   14.4   24.3   29.6   19.6  s8
+//      64, 4096 x 4096          20.1    9.9    9.9   15.4   17.7   14.2   21.8   16.8   25.8   30.8   21.9  s4
+//     256, 4096 x 4096          72.4   29.6   25.3   22.8   17.9   19.0   21.9   21.3   26.7   33.0   28.2  2/1
+//    1024, 4096 x 4096         282.2  103.4   90.2   82.9   35.7   52.2   26.5   42.0   31.1   35.7   34.6  4/1
+//    4096, 4096 x 4096          1119  397.4  348.7  317.1  136.5  192.4   98.9  148.0   94.5   84.2  126.9  8/1
+//      64, 16 of 4096 x 2048    63.0   28.5   25.5   24.5   23.9   29.2   24.2   29.8   24.7   31.7   33.4  s1
+//     128, 8 of 4096 x 4096     63.5   31.3   28.9   29.2   24.7   27.6   25.2   28.0   27.2   31.9   31.1  s2
+//     512, 8 of 4096 x 4096    189.6   73.9   62.0   60.3   38.8   43.1   30.8   41.5   30.3   34.0   36.0  4/1
+//    4096, 8 of 4096 x 4096     1341  469.5  371.7  336.4  161.6  293.0  124.0  206.0  101.7  111.8  159.3  6/1
+//    8192, 8 of 4096 x 4096     2661  924.1  720.3  650.5  304.4  535.6  218.5  413.9  188.9  189.2  316.1  8/1
+//      64, 128 of 2048 x 1024  103.9   34.4   24.5   20.4   22.7   28.4   23.5   29.8   25.1   28.2   33.9  s1
+//    1024, 128 of 2048 x 1024  303.8   89.4   60.0   50.7   52.8   79.9   53.7   76.4   55.0   61.5   89.5  s1
+//    8192, 128 of 2048 x 1024   1304  352.8  214.2  153.9  106.9  184.7   85.5  150.9   85.7   87.6  155.5  8/1
 // The gradient (no kernel of few rows):
-//     16, 4096 x 4096                         22.9   17.1   13.9   23.7   17.8   31.0   21.9  2/8: 13.4
-//    512, 4096 x 4096                         24.9   35.8   50.8   27.6   25.5   35.6   30.3  2/1
-//    512, 8 4096 x 4096                       70.3   67.2   74.9   47.6   55.2   50.9   42.6  8/2
-//   2048, 8 4096 x 2048                       66.5   80.1  118.5   52.1   62.4   38.1   56.6  8/1
+//   rows, matrices               2/1    2/2    2/4    2/8    4/1    4/2    6/1    6/2    8/1    8/2  rule
+//      16, 4096 x 4096          20.1   15.3   12.7   12.7   22.9   17.0   27.6   19.5   30.5   21.2  2/4
+//     512, 4096 x 4096          24.2   34.5   48.0   71.8   25.9   24.5   30.4   27.5   34.1   29.9  2/1
+//     512, 8 of 4096 x 4096     47.4   50.6   61.9   95.8   33.0   43.2   33.8   36.7   34.8   37.1  4/1
+//    2048, 8 of 4096 x 2048     66.9   79.3  103.7  160.9   51.4   60.1   35.1   51.5   38.9   62.7  6/1
+//    1024, 128 of 2048 x 1024   49.7   61.2   80.9  127.6   50.6   61.8   52.3   66.4   56.1   71.1  2/1
+// The choice is within 5% of the best of them but for 128 rows over 8 matrices (29.2
+// for 24.7) and 8192 over 128 (91.6 for 85.5).  Sizes of the matrices on both sides of
+// 64 MB, and matrices that the cache does not hold, were not compared.
 struct BlockShape {
     int nt;
     int64_t splits;

@@ -57,7 +57,13 @@ __device__ __forceinline__ float row_sum(float v, float* s) {
 // and rows of up to 8 KB have one, but where there are too few rows to fill the
 // device with (fewer than 2048: four waves each).  16421 rows of 4096 bf16 with the
 // residual to codes: 98 us, 473 MB at 4.8 TB/s; 8192 of 5120 f16 to f16: 62 us, 5.4
-// TB/s; 32 rows of 4096: 4.4 us, a load, a barrier and a store.
+// TB/s; 32 rows of 4096: 4.0 us, a load, a barrier and a store.
+//   bf16 to codes with the residual, in a graph, us with four waves a row / with one:
+//   rows            32        512       1024       2048        4096        8192
+//   of 1024   3.4 / 3.8  3.8 / 4.1  4.7 / 4.2  6.9 / 4.8  10.8 / 6.9  18.5 / 12.7
+//   of 2048   3.5 / 5.5  4.1 / 5.9  5.5 / 6.4  7.7 / 7.7  13.8 / 13.4 23.4 / 22.5
+//   of 4096   4.0 / 8.9  5.0 / 9.7  7.1 / 10.7 13.0 / 15.6 21.1 / 27.1 37.4 / 45.3
+// (the rows of 4096 are found in the memory-side cache there)
 template <typename T, int WPR, int NC, bool OUT8>
 __global__ __launch_bounds__(WPR == 1 ? 256 : 64 * WPR) void k_norm(
     const T* __restrict__ x, const T* __restrict__ res, int64_t Tn, int d, int C, const void* __restrict__ weight,
@@ -158,7 +164,9 @@ hipError_t launch_norm(DType xt, const void* x, int64_t T, int64_t d, const void
 // a lane keeps the weight gradient's sums of its columns in registers and
 // leaves them in part[b], which k_norm_grad_fold adds in the order of b.  Both sums
 // of a row (h^2 and u h) come from one reading of it.  8192 rows of 4096 bf16 with
-// the residual's gradient: 53 us, 268 MB at 5.1 TB/s, of which the fold takes 5.
+// the residual's gradient: 58 us, 268 MB at 4.6 TB/s, of which the fold takes 5 (in a
+// graph that repeats it 50); in such a graph 2048 rows of 16384 take 66 us, 4096 of
+// them 126 (4.3 TB/s), 2048 of 32768 176 (3.1 TB/s: what is spilled).
 template <typename T, int WPR, int NC, bool GW>
 __global__ __launch_bounds__(64 * WPR) void k_norm_grad(const T* __restrict__ grad, const T* __restrict__ hx, int64_t Tn,
                                                         int d, int C, const T* __restrict__ gres,
@@ -169,7 +177,9 @@ __global__ __launch_bounds__(64 * WPR) void k_norm_grad(const T* __restrict__ gr
     const int w = threadIdx.x >> 6, lane = threadIdx.x & 63;
     const int c0 = lane + 64 * w;
     // four chunks' weights are read again for every row: kept, they would cost registers
-    // that the rows need (spilled, two rows of 14016 took 34 us)
+    // that the rows need (two rows of 14016 took 34 us).  Blocks of 16 waves have 128
+    // registers a lane: with the weight's gradient, four chunks still spill 28 (f16) or 31
+    // (bf16) of them, two chunks of bf16 5
     constexpr bool KEEP = NC < 4;
     float wv[KEEP ? NC : 1][N], acc[NC][N];
     auto weights = [&](int i, float (&v)[N]) {
@@ -339,8 +349,8 @@ hipError_t launch_norm_grad(DType xt, const void* grad, const void* h, int64_t T
 }
 
 // Codes of rows by blocks of 128 columns: a thread a chunk, a row's chunks
-// filled up to whole blocks.  2048 rows of 4096 bf16: 7.6 us, 25 MB at 3.3 TB/s (one
-// chunk a thread: the launch's start and end weigh).
+// filled up to whole blocks.  2048 rows of 4096 bf16: 7.1 us, 25 MB at 3.5 TB/s, 6.3
+// in a graph that repeats it (one chunk a thread: the launch's start and end weigh).
 template <typename T>
 __global__ __launch_bounds__(256) void k_quantize_rows(const T* __restrict__ x, int64_t rows, int d, uint32_t C,
                                                        uint8_t* __restrict__ codes, float* __restrict__ scales, int nb,
@@ -371,7 +381,7 @@ __global__ __launch_bounds__(256) void k_quantize_rows(const T* __restrict__ x, 
 
 // Codes of matrices by blocks of 128 x 128: a block of threads each, a thread
 // the chunks of one column place in every 16th (float32: 8th) row.  Done once for
-// matrices that are held.
+// matrices that are held: 8 of 4096 x 4096 bf16 79 us, 403 MB at 5.1 TB/s.
 template <typename T>
 __global__ __launch_bounds__(256) void k_quantize_matrix(const T* __restrict__ x, int64_t M, int d, int C, int64_t mb,
                                                          uint8_t* __restrict__ codes, float* __restrict__ scales,

@@ -326,9 +326,13 @@ def kmeans_block_product(x, x_scales, codes, scales, offsets=None, order=None, d
     (or [M, K]), scales [E, ceil(M / 128), ceil(K / 128)].  order [S] int32 of
     kmeans_plan: x has T rows (S = T * top) and row p of the product is row
     order[p] // top of x, zeros for -1.  Returns [S, M] of `dtype` (None: x's, or
-    bfloat16 from codes); rows past offsets[E] are zeros.  Differentiable in x
-    where it is no codes (its rounding to codes is passed through); the matrices
-    are held."""
+    bfloat16 from codes); rows past offsets[E] are zeros.
+
+    Differentiable in x where it is no codes; the matrices are held.  The backward
+    pass is an 8-bit product too: the rounding of x to codes is passed through, the
+    gradient that comes in is itself rounded to codes (kmeans_block_product_grad),
+    and with an order every choice's row of the result is rounded to x's type
+    before a token's rows are added in float32."""
     dev = _rows_tensor(x, "x")
     E, M, K = _matrices(codes, scales, dev)
     T, top, S = x.shape[0], 1, x.shape[0]
@@ -445,7 +449,8 @@ class _BlockProduct(torch.autograd.Function):
         codes, scales, offsets, order = ctx.saved_tensors
         rows = kmeans_block_product_grad(grad.contiguous(), None, codes, scales, offsets, ctx.dtype)
         if order is not None:
-            # the rows back at the tokens that they were gathered from
+            # the rows back at the tokens that they were gathered from (of x's type, as a
+            # dispatched layer has them: half the bytes of float32 rows for 16-bit tokens)
             S = order.numel()
             if S == 0:
                 return rows.new_zeros((ctx.T, rows.shape[1])), *[None] * 7
